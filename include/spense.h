@@ -32,8 +32,8 @@
  *   - The library is not thread-safe per handle: at most one spense_linear may
  *     be in flight on a handle at a time (its split-K and gather workspaces
  *     are shared).
- *   - spense_linear, spense_linear_w8a8 and spense_glu may be captured in a HIP
- *     graph once an eager call on the same handle at a batch size of at least
+ *   - spense_linear, spense_linear_w8a8, spense_linear_w4a4, spense_glu and
+ *     spense_experts_linear may be captured in a HIP graph once an eager call on the same handle at a batch size of at least
  *     the captured one has run (automatic split counts): a call that has to
  *     grow the handle's workspaces synchronises the stream and allocates, and
  *     sizes them for every batch size up to its own, whatever split count the
@@ -56,7 +56,8 @@ extern "C" {
 typedef enum spense_dtype {
   SPENSE_F32 = 0,      /* IEEE binary32 */
   SPENSE_BF16 = 1,     /* bfloat16 */
-  SPENSE_FP8_E4M3 = 2  /* OCP e4m3fn: bias 7, largest finite 448, no infinities */
+  SPENSE_FP8_E4M3 = 2, /* OCP e4m3fn: bias 7, largest finite 448, no infinities */
+  SPENSE_MX4 = 3       /* microscaled e2m1: 32 consecutive columns share a power of two (spense_quantize_mx4) */
 } spense_dtype;
 
 typedef enum spense_status {
@@ -80,11 +81,14 @@ typedef struct spense_layer_info {
                              + dense block = N*(K_s/2*b + K_s/8 + K_d*b), b = element bytes */
   int64_t device_bytes;   /* bytes of the device-resident packed form, padding included */
   int32_t split;          /* 0: input-split layer (spense_pack); 1: output-split (spense_pack_rows);
-                             2: GLU block (spense_pack_glu) */
+                             2: GLU block (spense_pack_glu); 3: mx4 layer (spense_pack_mx4);
+                             4: experts' layers (spense_pack_experts) */
   int64_t N_s, N_d;       /* output-split: 2:4 rows / dense rows (input-split: N and 0); for an
                              output-split layer K_s = K when N_s > 0 and K_d = K when N_d > 0.
                              GLU block: N = K = H, N_s / N_d = 2:4 / dense intermediate indices,
-                             K_s / K_d those of the down projection */
+                             K_s / K_d those of the down projection.
+                             mx4 layer, experts' layers: N, K of one expert, K_d = K, N_s = experts,
+                             N_d = output columns (N / 2 of a gate/up layer); weight_bytes of all */
 } spense_layer_info;
 
 /*
@@ -330,6 +334,138 @@ int spense_quantize_tokens(const void* X, int64_t M, int64_t K, int64_t ldx, uin
  */
 int spense_linear_w8a8(spense_handle h, const void* X, int64_t M, int64_t ldx, void* Y, int32_t ydtype, int64_t ldy,
                        int32_t splits, void* stream);
+
+/*
+ * Microscaled 4-bit weights (mx4).
+ *
+ * An mx4 matrix of M rows and K columns is
+ *   codes   [M, ldc] bytes, ldc >= ceil(K/2): two e2m1 codes a byte, the even
+ *           column in the low half; a code is a sign bit above two exponent
+ *           bits and one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *   scales  [M, lds] bytes, lds >= ceil(K/32): columns 32b .. 32b+31 of a row
+ *           stand for code * 2^(scales[b] - 127); 255 makes them NaN.
+ *
+ * spense_quantize_mx4 - the mx4 matrix nearest to X.
+ *
+ * Per block of 32 consecutive columns (the last one may be shorter):
+ *   scale = clamp(floor(log2(max |x|)) - 2 + 127, 0, 254), 0 for a block of zeros,
+ *   code  = the e2m1 number nearest to x * 2^(127 - scale), ties to the even
+ *           code, magnitudes above 6 to 6, the sign kept;
+ * a block that holds a NaN or an infinity has scale 255 and codes 0.  Exact:
+ * the same bits as the formula in any precision.  The unused half of the last
+ * byte of an odd K is 0.
+ *
+ *   X       device pointer, [M, ldx] of xdtype (SPENSE_F32 or SPENSE_BF16), ldx >= K.
+ * 0 <= M <= 2^24, 1 <= K <= 2^20.  Asynchronous on `stream`.
+ */
+int spense_quantize_mx4(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, int64_t ldc,
+                        uint8_t* scales, int64_t lds, void* stream);
+
+/*
+ * spense_dequantize_mx4 - the numbers an mx4 matrix stands for, into Y [M, ldy] of
+ * ydtype (SPENSE_F32 or SPENSE_BF16; exact in both, down to the subnormals).
+ * Sizes as for spense_quantize_mx4.  Asynchronous on `stream`.
+ */
+int spense_dequantize_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t M, int64_t K,
+                          void* Y, int32_t ydtype, int64_t ldy, void* stream);
+
+/*
+ * spense_pack_mx4 - a linear layer with mx4 weights W[N,K] (once per weight).
+ *
+ * spense_linear runs it on bf16 activations, Y = X . W^T, with every product
+ * exact and the sum in fp32; spense_linear_w4a4 quantises the activations
+ * first.  spense_info and spense_free accept the handle;
+ * spense_linear_splits with a forced split count and spense_linear_noalloc
+ * return SPENSE_EUNSUPPORTED.  Synchronises `stream` before returning.
+ */
+int spense_pack_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t N, int64_t K,
+                    void* stream, spense_handle* out);
+
+/*
+ * spense_linear_w4a4 - Y = mx4(X) . W^T on a layer from spense_pack_mx4.
+ *
+ * X [M, ldx] bf16 is quantised as spense_quantize_mx4 does, into the handle's
+ * workspace; products are exact, the sum runs in fp32 in a fixed order.
+ * Y [M, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16).  1 <= M <= 2^24.
+ * Workspaces, asynchrony and graph capture as for spense_linear.
+ */
+int spense_linear_w4a4(spense_handle h, const void* X, int64_t M, int64_t ldx, void* Y, int32_t ydtype, int64_t ldy,
+                       void* stream);
+
+/*
+ * spense_pack_experts - the linear layers of E experts (once per set).
+ *
+ *   W        device pointer, the experts' matrices one after the other: [E*N, ldw]
+ *            bf16, ldw >= K, or mx4 codes [E*N, ldw bytes].
+ *   wdtype   SPENSE_BF16 or SPENSE_MX4 (SPENSE_EUNSUPPORTED for the others).
+ *   scales   mx4: [E*N, lds] bytes; NULL for bf16.
+ *   glu      0, or 1 for gate and up projections in one: N = 2I, rows [0, I) of an
+ *            expert the gate, rows [I, 2I) the up projection, and the layer
+ *            writes the I columns silu(gate) * up.
+ * 1 <= E <= 1024.  Synchronises `stream` before returning.
+ */
+int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, int64_t E, int64_t N, int64_t K,
+                        int64_t ldw, int64_t lds, int32_t glu, void* stream, spense_handle* out);
+
+/*
+ * spense_experts_linear - rows grouped by expert through their expert's layer:
+ *
+ *   Y[r] = X[rows ? rows[r] : r] . W_e^T   for offsets[e] <= r < offsets[e + 1]
+ *
+ * (or silu(gate) * up).  Only these rows of Y are written; an expert may have
+ * none of them, or all.
+ *
+ *   X        device pointer, [M, ldx] bf16, ldx >= K.
+ *   adtype   SPENSE_BF16: the activations as they are; SPENSE_MX4: quantised in the
+ *            call (mx4 weights only).
+ *   rows     device pointer, [R] int32 rows of X, or NULL (then M >= R); a row
+ *            outside [0, M) is taken as zeros.
+ *   offsets  device pointer, [E + 1] int32, ascending from 0 on; values past R count as R.
+ *   R        grouped rows that rows and Y have room for, 0 <= R <= 2^24.
+ *   Y        device pointer, [R, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16), ldy >= N (I).
+ * The sizes of the groups stay on the device.  Deterministic; workspaces,
+ * asynchrony and graph capture as for spense_linear (R and M at most those of
+ * the eager call, with the same adtype and with rows given or not).
+ */
+int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_t M, int64_t ldx, const int32_t* rows,
+                          const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, void* stream);
+
+/*
+ * spense_route - the experts of every token, and the tokens grouped by expert.
+ *
+ *   logits   device pointer, [T, ldl] of ltype (SPENSE_F32 or SPENSE_BF16), ldl >= E.
+ *   k        choices per token, 1 <= k <= E <= 1024; T*k <= 2^24, T may be 0.
+ *   ids      [T, k] int32: the experts with the largest logits, largest first,
+ *            equal ones lower expert first.  NaN and -inf logits are never
+ *            taken; a token with fewer than k others has -1 in the missing places.
+ *   weights  [T, k] float32: softmax weights, over the token's choices
+ *            (renormalize != 0) or over all its logits; 0 in missing places.
+ *            +inf logits share the weight equally.
+ *   offsets  [E + 1] int32, rows [T*k] int32, pos [T, k] int32: the pairs (token,
+ *            choice) grouped by expert, in token order; row r of expert e,
+ *            offsets[e] <= r < offsets[e + 1], is token rows[r], and choice j of
+ *            token t is row pos[t, j] (-1: missing).  rows is -1 past offsets[E].
+ *   work     spense_route_workspace(T, E, k) bytes, 4-byte aligned, may be NULL if 0.
+ * All device pointers.  Deterministic, asynchronous on `stream`, graph-capturable,
+ * no state kept: calls with workspaces of their own may overlap.
+ */
+int64_t spense_route_workspace(int64_t T, int64_t E, int32_t k);
+int spense_route(const void* logits, int32_t ltype, int64_t T, int64_t E, int64_t ldl, int32_t k, int32_t renormalize,
+                 int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* work, void* stream);
+
+/*
+ * spense_experts_combine - Y[t] = sum_j weights[t, j] * O[pos[t, j]], the
+ * experts' outputs weighted and brought back to their tokens.
+ *
+ *   O        device pointer, [R, ldo] of otype (SPENSE_F32 or SPENSE_BF16), ldo >= N.
+ *   pos, weights  device pointers, [T, k] (from spense_route); a pos outside
+ *            [0, R) adds nothing.
+ *   Y        device pointer, [T, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16), ldy >= N.
+ * Summed in fp32 in the order of j, rounded once.  Asynchronous on `stream`.
+ */
+int spense_experts_combine(const void* O, int32_t otype, int64_t R, int64_t ldo, const int32_t* pos,
+                           const float* weights, int64_t T, int32_t k, int64_t N, void* Y, int32_t ydtype, int64_t ldy,
+                           void* stream);
 
 /* spense_info - sizes of a packed layer (host-side, no synchronisation). */
 int spense_info(spense_handle h, spense_layer_info* info);

@@ -39,11 +39,24 @@ written from the definitions on the pages:
     explainer's Technical summary 1): 2:4 means at most two nonzeros in every
     four consecutive weights.
 
-Parity status: every function is pinned by ``tests/test_oracle.py`` (closed
-forms, exhaustive brute force on tiny inputs, library routines for the
-special cases).  No function is "parity unpinned".
+The microscaled 4-bit format, the experts' layers and the router
+(``experts.py``) are not on the pages; they are written from their formulas.
+
+Parity status: every function is pinned by ``tests/test_oracle.py`` or
+``tests/test_experts_oracle.py`` (closed forms, exhaustive brute force on tiny
+inputs, library routines for the special cases).  No function is "parity
+unpinned".
 """
 
+from .experts import (  # noqa: F401
+    combine_ref,
+    experts_linear_ref,
+    mx4_quantize_ref,
+    mx4_values_ref,
+    nearest_e2m1,
+    product_ref,
+    route_ref,
+)
 from .spense import (  # noqa: F401
     DT_BF16,
     DT_F32,

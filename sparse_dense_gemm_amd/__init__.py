@@ -19,6 +19,7 @@ import numpy as np
 DT_F32 = 0
 DT_BF16 = 1
 DT_FP8 = 2
+DT_MX4 = 3
 
 SPENSE_OK = 0
 SPENSE_EINVAL = -1
@@ -83,6 +84,24 @@ def _lib():
     lib.spense_linear_w8a8.restype = ctypes.c_int
     lib.spense_linear_w8a8.argtypes = [vp, vp, i64, i64, vp, i32, i64, i32, vp]
     lib.spense_linear_splits.restype = ctypes.c_int
+    lib.spense_quantize_mx4.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]
+    lib.spense_quantize_mx4.restype = ctypes.c_int
+    lib.spense_dequantize_mx4.argtypes = [vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]
+    lib.spense_dequantize_mx4.restype = ctypes.c_int
+    lib.spense_pack_mx4.argtypes = [vp, i64, vp, i64, i64, i64, vp, ctypes.POINTER(vp)]
+    lib.spense_pack_mx4.restype = ctypes.c_int
+    lib.spense_linear_w4a4.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    lib.spense_linear_w4a4.restype = ctypes.c_int
+    lib.spense_pack_experts.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, i32, vp, ctypes.POINTER(vp)]
+    lib.spense_pack_experts.restype = ctypes.c_int
+    lib.spense_experts_linear.argtypes = [vp, vp, i32, i64, i64, vp, vp, i64, vp, i32, i64, vp]
+    lib.spense_experts_linear.restype = ctypes.c_int
+    lib.spense_route_workspace.argtypes = [i64, i64, i32]
+    lib.spense_route_workspace.restype = i64
+    lib.spense_route.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.spense_route.restype = ctypes.c_int
+    lib.spense_experts_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i32, i64, vp]
+    lib.spense_experts_combine.restype = ctypes.c_int
     lib.spense_info.argtypes = [vp, ctypes.POINTER(LayerInfo)]
     lib.spense_info.restype = ctypes.c_int
     lib.spense_export.argtypes = [vp, vp, vp, vp, vp, vp, vp]
@@ -308,6 +327,123 @@ def spense_linear_w8a8(h: int, X, Y, *, splits: int = 0, ydtype: Optional[int] =
     _check(st, "spense_linear_w8a8")
 
 
+def spense_quantize_mx4(X, codes, scales, *, xdtype: Optional[int] = None, stream=None) -> None:
+    """mx4 form of X [M, K]: codes (uint8 [M, >= (K+1)/2]) and exponent bytes (uint8 [M, >= ceil(K/32)])."""
+    xdtype = dtype_of(X) if xdtype is None else xdtype
+    M, K = X.shape
+    _mx4_shape(codes, scales, M, K)
+    st = _lib().spense_quantize_mx4(X.data_ptr(), xdtype, M, K, X.stride(0), codes.data_ptr(), codes.stride(0),
+                                    scales.data_ptr(), scales.stride(0), _stream(stream))
+    _check(st, "spense_quantize_mx4")
+
+
+def spense_dequantize_mx4(codes, scales, Y, *, ydtype: Optional[int] = None, stream=None) -> None:
+    """The numbers an mx4 matrix stands for, into Y [M, K] (float32 or bfloat16)."""
+    ydtype = dtype_of(Y) if ydtype is None else ydtype
+    M, K = Y.shape
+    _mx4_shape(codes, scales, M, K)
+    st = _lib().spense_dequantize_mx4(codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), M, K,
+                                      Y.data_ptr(), ydtype, Y.stride(0), _stream(stream))
+    _check(st, "spense_dequantize_mx4")
+
+
+def _mx4_shape(codes, scales, rows: int, K: int) -> None:
+    if (codes.shape[0] < rows or scales.shape[0] < rows or codes.shape[1] < (K + 1) // 2
+            or scales.shape[1] < (K + 31) // 32):
+        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold {rows} x {K} mx4")
+    for t in (codes, scales):
+        if t.element_size() != 1 or t.stride(1) != 1:
+            raise ValueError("codes and scales are bytes, contiguous along a row")
+
+
+def spense_pack_mx4(codes, scales, *, N: Optional[int] = None, K: Optional[int] = None, stream=None) -> int:
+    """Pack an mx4 weight matrix [N, K] (K: twice the code bytes of a row unless given); returns the handle."""
+    N = codes.shape[0] if N is None else N
+    K = 2 * codes.shape[1] if K is None else K
+    _mx4_shape(codes, scales, N, K)
+    h = ctypes.c_void_p()
+    st = _lib().spense_pack_mx4(codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), N, K,
+                                _stream(stream), ctypes.byref(h))
+    _check(st, "spense_pack_mx4")
+    return h.value
+
+
+def spense_linear_w4a4(h: int, X, Y, *, M: Optional[int] = None, stream=None) -> None:
+    """Y = mx4(X) . W^T on an mx4 layer (asynchronous on the stream)."""
+    st = _lib().spense_linear_w4a4(h, X.data_ptr(), X.shape[0] if M is None else M, X.stride(0), Y.data_ptr(),
+                                   dtype_of(Y), Y.stride(0), _stream(stream))
+    _check(st, "spense_linear_w4a4")
+
+
+def spense_pack_experts(W, wdtype: Optional[int] = None, *, scales=None, K: Optional[int] = None, glu: bool = False,
+                        stream=None) -> int:
+    """Pack experts' weights: W bf16 [E, N, K], or mx4 codes [E, N, bytes] with exponent bytes [E, N, ceil(K/32)]."""
+    wdtype = dtype_of(W) if wdtype is None else wdtype
+    E, N = W.shape[0], W.shape[1]
+    if K is None:
+        K = 2 * W.shape[2] if wdtype == DT_MX4 else W.shape[2]
+    W2 = _rows_in_line(W)
+    s2 = None if scales is None else _rows_in_line(scales)
+    if wdtype == DT_MX4 and s2 is not None:
+        _mx4_shape(W2, s2, E * N, K)
+    h = ctypes.c_void_p()
+    st = _lib().spense_pack_experts(W2.data_ptr(), wdtype, _ptr(s2), E, N, K, W2.stride(0),
+                                    0 if s2 is None else s2.stride(0), int(glu), _stream(stream), ctypes.byref(h))
+    _check(st, "spense_pack_experts")
+    return h.value
+
+
+def _rows_in_line(t):
+    """[E, N, C] as [E * N, C] without a copy."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1)):
+        raise ValueError("experts' matrices are [E, N, columns], one after the other, contiguous along a row")
+    return t.as_strided((t.shape[0] * t.shape[1], t.shape[2]), (t.stride(1), 1))
+
+
+def spense_experts_linear(h: int, X, offsets, Y, *, rows=None, adtype: int = DT_BF16, R: Optional[int] = None,
+                          stream=None) -> None:
+    """Rows of X grouped by expert (offsets int32 [E + 1], rows int32 [R] if X is not grouped itself) into Y [R, ...]."""
+    R = Y.shape[0] if R is None else R
+    st = _lib().spense_experts_linear(h, X.data_ptr(), adtype, X.shape[0], X.stride(0),
+                                      None if rows is None else rows.data_ptr(), offsets.data_ptr(), R, Y.data_ptr(),
+                                      dtype_of(Y), Y.stride(0), _stream(stream))
+    _check(st, "spense_experts_linear")
+
+
+def spense_route_workspace(T: int, E: int, k: int) -> int:
+    """Bytes of workspace spense_route needs."""
+    n = _lib().spense_route_workspace(T, E, k)
+    if n < 0:
+        _check(int(n), "spense_route_workspace")
+    return n
+
+
+def spense_route(logits, k: int, ids, weights, offsets, rows, pos, work=None, *, renormalize: bool = True,
+                 stream=None) -> None:
+    """Experts of every token (ids int32, weights float32 [T, k]) and the tokens grouped by expert
+    (offsets int32 [E + 1], rows int32 [T * k], pos int32 [T, k])."""
+    T, E = logits.shape
+    if ids.numel() < T * k or weights.numel() < T * k or rows.numel() < T * k or pos.numel() < T * k \
+            or offsets.numel() < E + 1:
+        raise ValueError("ids, weights, rows and pos hold T * k values, offsets E + 1")
+    need = spense_route_workspace(T, E, k)
+    if need and (work is None or work.numel() * work.element_size() < need):
+        raise ValueError(f"spense_route needs {need} bytes of workspace")
+    st = _lib().spense_route(logits.data_ptr(), dtype_of(logits), T, E, logits.stride(0), k, int(renormalize),
+                             ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
+                             None if work is None else work.data_ptr(), _stream(stream))
+    _check(st, "spense_route")
+
+
+def spense_experts_combine(O, pos, weights, Y, *, stream=None) -> None:
+    """Y[t] = sum_j weights[t, j] O[pos[t, j]]."""
+    T, k = pos.shape
+    st = _lib().spense_experts_combine(O.data_ptr(), dtype_of(O), O.shape[0], O.stride(0), pos.data_ptr(),
+                                       weights.data_ptr(), T, k, Y.shape[1], Y.data_ptr(), dtype_of(Y), Y.stride(0),
+                                       _stream(stream))
+    _check(st, "spense_experts_combine")
+
+
 def spense_info(h: int) -> dict:
     info = LayerInfo()
     _check(_lib().spense_info(h, ctypes.byref(info)), "spense_info")
@@ -331,16 +467,10 @@ def spense_abi_version() -> int:
     return _lib().spense_abi_version()
 
 
-class SpenseLinear:
-    """Owns one packed layer; ``layer(X, Y)`` runs spense_linear."""
+class _Owned:
+    """Owns a packed layer's handle."""
 
-    def __init__(self, W, wdtype: Optional[int] = None, **kw):
-        self.handle = spense_pack(W, wdtype, **kw)
-        self.info = spense_info(self.handle)
-
-    def __call__(self, X, Y, splits: int = 0, stream=None):
-        spense_linear_splits(self.handle, X, Y, splits, stream=stream)
-        return Y
+    handle = None
 
     def close(self):
         if self.handle:
@@ -352,3 +482,43 @@ class SpenseLinear:
             self.close()
         except Exception:
             pass
+
+
+class SpenseLinear(_Owned):
+    """Owns one packed layer; ``layer(X, Y)`` runs spense_linear."""
+
+    def __init__(self, W, wdtype: Optional[int] = None, **kw):
+        self.handle = spense_pack(W, wdtype, **kw)
+        self.info = spense_info(self.handle)
+
+    def __call__(self, X, Y, splits: int = 0, stream=None):
+        spense_linear_splits(self.handle, X, Y, splits, stream=stream)
+        return Y
+
+
+class SpenseLinearMx4(_Owned):
+    """Owns one packed mx4 layer; ``layer(X, Y)`` runs spense_linear, ``layer.w4a4(X, Y)`` spense_linear_w4a4."""
+
+    def __init__(self, codes, scales, **kw):
+        self.handle = spense_pack_mx4(codes, scales, **kw)
+        self.info = spense_info(self.handle)
+
+    def __call__(self, X, Y, stream=None):
+        spense_linear(self.handle, X, Y, stream=stream)
+        return Y
+
+    def w4a4(self, X, Y, stream=None):
+        spense_linear_w4a4(self.handle, X, Y, stream=stream)
+        return Y
+
+
+class SpenseExperts(_Owned):
+    """Owns the packed layers of a set of experts; ``experts(X, offsets, Y, rows=...)`` runs spense_experts_linear."""
+
+    def __init__(self, W, wdtype: Optional[int] = None, **kw):
+        self.handle = spense_pack_experts(W, wdtype, **kw)
+        self.info = spense_info(self.handle)
+
+    def __call__(self, X, offsets, Y, *, rows=None, adtype: int = DT_BF16, stream=None):
+        spense_experts_linear(self.handle, X, offsets, Y, rows=rows, adtype=adtype, stream=stream)
+        return Y

@@ -16,6 +16,7 @@
 
 #include "../../include/spense.h"
 #include "spense_internal.h"
+#include "spense_mx.h"
 
 using namespace spense;
 
@@ -44,7 +45,9 @@ struct spense_layer {
   // output-split layer (Technical Summary 2.A): no packed form of its own;
   // part[0] holds the 2:4 rows (no dense columns), part[1] the dense rows (no
   // sparse columns); either may be absent.  rho_host = [sparse rows | dense rows].
-  int split = 0;  // 0 input-split layer, 1 output-split layer, 2 GLU block
+  // 0 input-split layer, 1 output-split layer, 2 GLU block, 3 mx4 layer, 4 experts' layers
+  int split = 0;
+  ExpertsLayer* experts = nullptr;  // mx4 layer, experts' layers: their packed form
   spense_layer* part[2] = {nullptr, nullptr};
   spense_layer* down = nullptr;  // GLU block: the down projection (input-split, read in rho order)
   int64_t N_s = 0, N_d = 0;
@@ -70,6 +73,7 @@ void release(spense_layer* h) {
   release(h->part[0]);
   release(h->part[1]);
   release(h->down);
+  experts_release(h->experts);
   void* ptrs[] = {h->wpack, h->scales, h->pi,      h->pip, h->vals32, h->meta32,
                   h->dense32, h->ws,   h->counters, h->xws, h->ycol,   h->wrow};
   for (void* p : ptrs)
@@ -120,6 +124,8 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 int32_t y_vec_ok(const void* Y, int64_t ldy) { return aligned16(Y) && ldy % 4 == 0 ? 1 : 0; }
 
 }  // namespace
+
+int spense::report_hip(hipError_t e) { return hip_fail(e); }
 
 extern "C" {
 
@@ -985,12 +991,52 @@ static int layer_parts(spense_layer* h, spense_layer* parts[2]) {
   return n;
 }
 
+// Sizes of an mx4 matrix: M rows of K columns, row strides of codes and scales in bytes.
+static bool mx4_matrix_ok(int64_t M, int64_t K, int64_t ldc, int64_t lds) {
+  return M >= 0 && M <= (int64_t(1) << 24) && K >= 1 && K <= (int64_t(1) << 20) && ldc >= (K + 1) / 2 &&
+         lds >= (K + kMxBlock - 1) / kMxBlock;
+}
+
+constexpr int64_t kMaxExperts = 1024;
+
+static bool route_sizes_ok(int64_t T, int64_t E, int64_t k) {
+  return T >= 0 && T <= (int64_t(1) << 24) && E >= 1 && E <= kMaxExperts && k >= 1 && k <= E &&
+         T * k <= (int64_t(1) << 24);
+}
+
+// A handle that holds packed experts (split: 3 one mx4 matrix, 4 a set).
+static int new_experts(const void* W, int32_t wdtype, const uint8_t* scales, int64_t E, int64_t N, int64_t K,
+                       int64_t ldw, int64_t lds, int32_t glu, int split, void* stream, spense_handle* out) {
+  spense_layer* h = new (std::nothrow) spense_layer();
+  if (!h) return SPENSE_ENOMEM;
+  h->split = split;
+  const int rc = experts_pack(W, wdtype, scales, E, N, K, ldw, lds, glu, (hipStream_t)stream, &h->experts);
+  if (rc != SPENSE_OK) release(h);
+  else *out = h;
+  return rc;
+}
+
+// The mx4 layer with activations left in bf16 or quantised (adtype).
+static int mx4_linear_call(spense_handle h, const void* X, int32_t xdtype, int32_t adtype, int64_t M, int64_t ldx,
+                           void* Y, int32_t ydtype, int64_t ldy, void* stream) {
+  const ExpertsDesc& d = experts_desc(h->experts);
+  if (M < 1 || M > (int64_t(1) << 24) || ldx < d.K || ldy < d.N) return SPENSE_EINVAL;
+  if (ldx >= kMaxLd) return SPENSE_EUNSUPPORTED;
+  if (!valid_dtype(xdtype) || !valid_dtype(ydtype)) return SPENSE_EINVAL;
+  if (xdtype != SPENSE_BF16 || ydtype == SPENSE_FP8_E4M3) return SPENSE_EUNSUPPORTED;
+  return experts_run(h->experts, X, adtype, M, ldx, nullptr, nullptr, M, Y, ydtype, ldy, (hipStream_t)stream);
+}
+
 // spense_linear_splits and spense_linear_noalloc: validation, then the launch
 // with the handle's workspaces or the fixed scratch.
 static int linear_call(spense_handle h, const void* X, int32_t xdtype, int64_t M, int64_t ldx, void* Y,
                        int32_t ydtype, int64_t ldy, int32_t splits, void* stream, bool noalloc) {
   if (!h || !X || !Y) return SPENSE_EINVAL;
-  if (h->split == 2) return SPENSE_EINVAL;  // a GLU block runs through spense_glu
+  if (h->split == 2 || h->split == 4) return SPENSE_EINVAL;  // spense_glu, spense_experts_linear
+  if (h->split == 3) {  // no split-K factor to force, no form that allocates nothing
+    if (noalloc || splits != 0) return SPENSE_EUNSUPPORTED;
+    return mx4_linear_call(h, X, xdtype, SPENSE_BF16, M, ldx, Y, ydtype, ldy, stream);
+  }
   const LayerDesc& d = h->d;
   if (M < 1 || M > (int64_t(1) << 24) || ldx < d.K || ldy < d.N) return SPENSE_EINVAL;
   if (ldx >= kMaxLd) return SPENSE_EUNSUPPORTED;
@@ -1194,6 +1240,11 @@ int spense_select_dense(const float* score, int64_t n, int64_t k, int32_t* dense
 int spense_info(spense_handle h, spense_layer_info* info) {
   if (!h || !info) return SPENSE_EINVAL;
   std::memset(info, 0, sizeof(*info));
+  info->split = h->split;
+  if (h->experts) {
+    experts_info(h->experts, info);
+    return SPENSE_OK;
+  }
   info->N = h->d.N;
   info->K = h->d.K;
   info->K_s = h->d.K_s;
@@ -1239,6 +1290,104 @@ int spense_free(spense_handle h) {
   if (!h) return SPENSE_EINVAL;
   release(h);
   return SPENSE_OK;
+}
+
+int spense_quantize_mx4(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, int64_t ldc,
+                        uint8_t* scales, int64_t lds, void* stream) {
+  if (!X || !codes || !scales || !mx4_matrix_ok(M, K, ldc, lds) || ldx < K) return SPENSE_EINVAL;
+  if (xdtype != SPENSE_F32 && xdtype != SPENSE_BF16)
+    return xdtype == SPENSE_FP8_E4M3 || xdtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
+  if (M == 0) return SPENSE_OK;
+  const hipError_t e = launch_mx4_quantize(X, xdtype, M, K, ldx, codes, ldc, scales, lds, (hipStream_t)stream);
+  return e == hipSuccess ? SPENSE_OK : hip_fail(e);
+}
+
+int spense_dequantize_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t M, int64_t K,
+                          void* Y, int32_t ydtype, int64_t ldy, void* stream) {
+  if (!codes || !scales || !Y || !mx4_matrix_ok(M, K, ldc, lds) || ldy < K) return SPENSE_EINVAL;
+  if (ydtype != SPENSE_F32 && ydtype != SPENSE_BF16)
+    return ydtype == SPENSE_FP8_E4M3 || ydtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
+  if (M == 0) return SPENSE_OK;
+  const hipError_t e = launch_mx4_dequantize(codes, ldc, scales, lds, M, K, Y, ydtype, ldy, (hipStream_t)stream);
+  return e == hipSuccess ? SPENSE_OK : hip_fail(e);
+}
+
+int spense_pack_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t N, int64_t K,
+                    void* stream, spense_handle* out) {
+  if (!out) return SPENSE_EINVAL;
+  *out = nullptr;
+  if (!codes || !scales || N < 1 || !mx4_matrix_ok(N, K, ldc, lds)) return SPENSE_EINVAL;
+  return new_experts(codes, SPENSE_MX4, scales, 1, N, K, ldc, lds, 0, 3, stream, out);
+}
+
+int spense_linear_w4a4(spense_handle h, const void* X, int64_t M, int64_t ldx, void* Y, int32_t ydtype, int64_t ldy,
+                       void* stream) {
+  if (!h || !X || !Y) return SPENSE_EINVAL;
+  if (h->split != 3) return SPENSE_EUNSUPPORTED;
+  return mx4_linear_call(h, X, SPENSE_BF16, SPENSE_MX4, M, ldx, Y, ydtype, ldy, stream);
+}
+
+int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, int64_t E, int64_t N, int64_t K,
+                        int64_t ldw, int64_t lds, int32_t glu, void* stream, spense_handle* out) {
+  if (!out) return SPENSE_EINVAL;
+  *out = nullptr;
+  if (!W || E < 1 || E > kMaxExperts || N < 1 || (glu && N % 2)) return SPENSE_EINVAL;
+  if (wdtype == SPENSE_F32 || wdtype == SPENSE_FP8_E4M3) return SPENSE_EUNSUPPORTED;
+  if (wdtype == SPENSE_MX4) {
+    if (!scales || !mx4_matrix_ok(N, K, ldw, lds)) return SPENSE_EINVAL;
+  } else if (wdtype == SPENSE_BF16) {
+    if (scales || !mx4_matrix_ok(N, K, ldw, kMaxLd) || ldw < K) return SPENSE_EINVAL;
+  } else {
+    return SPENSE_EINVAL;
+  }
+  return new_experts(W, wdtype, scales, E, N, K, ldw, lds, glu, 4, stream, out);
+}
+
+int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_t M, int64_t ldx, const int32_t* rows,
+                          const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, void* stream) {
+  if (!h || h->split != 4 || !X || !offsets || !Y) return SPENSE_EINVAL;
+  const ExpertsDesc& d = experts_desc(h->experts);
+  if (M < 0 || M > (int64_t(1) << 24) || R < 0 || R > (int64_t(1) << 24) || (!rows && M < R)) return SPENSE_EINVAL;
+  if (ldx < d.K || ldy < (d.glu ? d.N / 2 : d.N)) return SPENSE_EINVAL;
+  if (adtype != SPENSE_BF16 && adtype != SPENSE_MX4)
+    return valid_dtype(adtype) ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
+  if (ydtype != SPENSE_F32 && ydtype != SPENSE_BF16)
+    return ydtype == SPENSE_FP8_E4M3 || ydtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
+  if (ldx >= kMaxLd || (adtype == SPENSE_MX4 && d.wdtype != SPENSE_MX4)) return SPENSE_EUNSUPPORTED;
+  if (R == 0 || M == 0) return SPENSE_OK;
+  return experts_run(h->experts, X, adtype, M, ldx, rows, offsets, R, Y, ydtype, ldy, (hipStream_t)stream);
+}
+
+int64_t spense_route_workspace(int64_t T, int64_t E, int32_t k) {
+  if (!route_sizes_ok(T, E, k)) return SPENSE_EINVAL;
+  return route_work_bytes(T, E);
+}
+
+int spense_route(const void* logits, int32_t ltype, int64_t T, int64_t E, int64_t ldl, int32_t k, int32_t renormalize,
+                 int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* work,
+                 void* stream) {
+  if (!route_sizes_ok(T, E, k) || ldl < E || !offsets) return SPENSE_EINVAL;
+  if (ltype != SPENSE_F32 && ltype != SPENSE_BF16)
+    return ltype == SPENSE_FP8_E4M3 || ltype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
+  if (T > 0 && (!logits || !ids || !weights || !rows || !pos)) return SPENSE_EINVAL;
+  if (route_work_bytes(T, E) > 0 && (!work || ((uintptr_t)work & 3u))) return SPENSE_EINVAL;
+  const RouteArgs a{logits, ltype, T, E, ldl, k, renormalize, ids, weights, offsets, rows, pos, (int32_t*)work};
+  const hipError_t e = launch_route(a, (hipStream_t)stream);
+  return e == hipSuccess ? SPENSE_OK : hip_fail(e);
+}
+
+int spense_experts_combine(const void* O, int32_t otype, int64_t R, int64_t ldo, const int32_t* pos,
+                           const float* weights, int64_t T, int32_t k, int64_t N, void* Y, int32_t ydtype, int64_t ldy,
+                           void* stream) {
+  if (!O || !pos || !weights || !Y) return SPENSE_EINVAL;
+  if (T < 0 || T > (int64_t(1) << 24) || R < 0 || R > (int64_t(1) << 24) || k < 1 || k > kMaxExperts) return SPENSE_EINVAL;
+  if (N < 1 || N >= kMaxLd || ldo < N || ldy < N) return SPENSE_EINVAL;
+  for (const int32_t t : {otype, ydtype})
+    if (t != SPENSE_F32 && t != SPENSE_BF16)
+      return t == SPENSE_FP8_E4M3 || t == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
+  if (T == 0) return SPENSE_OK;
+  const hipError_t e = launch_combine(O, otype, R, ldo, pos, weights, T, k, N, Y, ydtype, ldy, (hipStream_t)stream);
+  return e == hipSuccess ? SPENSE_OK : hip_fail(e);
 }
 
 }  // extern "C"

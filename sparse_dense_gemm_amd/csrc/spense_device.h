@@ -1,9 +1,12 @@
 // Device helpers shared by the HIP kernel translation units of the Spense
-// linear layer (spense_kernels.hip, spense_tile.hip): element conversions,
-// the structured-sparse matrix instructions, buffer loads, the split-K
-// hand-off and the epilogue.  Everything here is inline and file-local to
-// each translation unit that includes it.
+// linear layer (spense_kernels.hip, spense_tile.hip) and of the microscaled and
+// expert products (spense_experts.hip): element conversions, the
+// structured-sparse matrix instructions, buffer loads, copies into LDS, the
+// split-K hand-off and the epilogue.  Everything here is inline and file-local
+// to each translation unit that includes it.
 #pragma once
+
+#include <type_traits>
 
 #include "spense_internal.h"
 
@@ -403,6 +406,60 @@ __device__ __forceinline__ i32x8 lds_b8(const uint8_t* p) {
 
 __device__ __forceinline__ f32x4 smfmac_fp8(const u32x4& a, const i32x8& b, const f32x4& c, int idx) {
   return __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(__builtin_bit_cast(i32x4, a), b, c, idx, 0, 0);
+}
+
+// Buffer descriptor words (the layout make_rsrc builds: base, no stride,
+// num_records bytes, raw-buffer flags), uniform across the wave.
+__device__ __forceinline__ i32x4 rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t a = (uint64_t)base;
+  i32x4 r;
+  r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF);
+  r.z = __builtin_amdgcn_readfirstlane((int)bytes);
+  r.w = 0x00020000;
+  return r;
+}
+
+// LDS byte address of a pointer into a __shared__ array
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Copies into LDS (buffer loads with an LDS destination): lane l's 16 (or 4)
+// bytes at voff + soff of the resource land at LDS address lds + 16 l (4 l);
+// offsets beyond the resource write zeros.  They are written as assembly so
+// that the compiler does not track them: it would otherwise wait for copies
+// into other stage buffers before LDS reads whenever more copies are in
+// flight than it follows one by one.  The kernel waits for them itself (a
+// counted s_waitcnt before each stage's barrier).  The s_nop is the wait
+// state between a write of m0 and an LDS copy, which the compiler does not
+// add for assembly.  NT: non-temporal cache policy.
+template <bool NT>
+__device__ __forceinline__ void copy16(const i32x4& r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  if constexpr (NT)
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+  else
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+}
+template <bool NT>
+__device__ __forceinline__ void copy4(const i32x4& r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  if constexpr (NT)
+    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen nt lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+  else
+    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+}
+
+// f(integral_constant<A>), ..., f(integral_constant<B - 1>), in order
+template <int A, int B, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (A < B) {
+    f(std::integral_constant<int, A>{});
+    static_for<A + 1, B>(f);
+  }
 }
 
 }  // namespace

@@ -1,0 +1,498 @@
+// HIP kernel of the products with packed mx4 or bf16 weights, for one weight
+// matrix (the mx4 linear layer) or a set of experts whose activation rows are
+// grouped by expert in runs of any length.
+//
+//   Y[r, n] = sum_k x[r, k] w_e[n, k],   o_e <= r < o_(e+1),
+//
+// with w (and x, if quantised) = code * 2^(exponent) in blocks of 32 columns.
+// Products of two mx4 blocks run on the scaled matrix instruction 16x16x128,
+// which takes the codes and the exponent bytes as they are stored; with bf16
+// activations mx4 weights are widened exactly in registers and, like bf16
+// weights, run on 16x16x32.  Sums are held in 32 bits.
+//
+// A workgroup owns NW R row tiles (16 R NW output columns) and up to 16 T
+// activation rows of one expert.  Weights are read once per workgroup, each
+// wave streaming its own row tiles from memory through a ring of D stages in
+// registers (they are packed as the matrix instructions' operands, so they
+// need neither LDS nor a shuffle); activations are shared by the waves, so
+// they are copied into LDS, C stages at a time into one of two buffers while
+// the other is read.  A stage is 256 bytes of every row: 128 bf16 columns or
+// 512 mx4 columns, in both cases four operands of 16 bytes per lane.
+#include "spense_device.h"
+#include "spense_mx.h"
+
+namespace spense {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Configurations: X(index, waves, row tiles per wave R, m-tiles T, stages per
+// LDS buffer C, ring depth D in stages, waves per SIMD the registers allow)
+#define SPENSE_EXPERT_CONFIGS(X) \
+  X(0, 8, 1, 1, 4, 4, 2)         \
+  X(1, 8, 1, 2, 4, 4, 2)         \
+  X(2, 4, 2, 4, 2, 2, 2)         \
+  X(3, 4, 2, 8, 1, 2, 1)         \
+  X(4, 4, 4, 16, 1, 2, 1)
+
+// First of the 16 rows and expert of m-tile group j (groups of `rows` rows,
+// counted over the experts in order); cnt = 0 where there is no such group.
+__device__ __forceinline__ void find_group(const ExpertsDesc& d, const ExpertsArgs& a, int rows, int j, int& e,
+                                           int64_t& row0, int& cnt) {
+  if (!a.offsets) {
+    e = 0;
+    row0 = (int64_t)j * rows;
+    const int64_t left = a.R - row0;
+    cnt = (int)(left <= 0 ? 0 : left < rows ? left : rows);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;  // groups of the experts before this chunk of 64
+  e = 0;
+  row0 = 0;
+  cnt = 0;
+  for (int64_t base = 0; base < d.E; base += 64) {
+    const int64_t i = base + lane;
+    int64_t lo = 0, hi = 0;
+    if (i < d.E) {
+      lo = a.offsets[i];
+      hi = a.offsets[i + 1];
+      lo = lo < 0 ? 0 : lo > a.R ? a.R : lo;
+      hi = hi < lo ? lo : hi > a.R ? a.R : hi;
+    }
+    const int n = (int)((hi - lo + rows - 1) / rows);
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o);
+      if (lane >= o) incl += up;
+    }
+    const int excl = before + incl - n;
+    const uint64_t hit = __ballot(j >= excl && j < excl + n);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      const int k = j - __builtin_amdgcn_readlane(excl, src);
+      const int l0 = __builtin_amdgcn_readlane((int)lo, src), h0 = __builtin_amdgcn_readlane((int)hi, src);
+      e = (int)base + src;
+      row0 = (int64_t)l0 + (int64_t)k * rows;
+      const int left = h0 - (int)row0;
+      cnt = left < rows ? left : rows;
+      return;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+}
+
+// exponent byte -> the power of two (255 -> NaN)
+__device__ __forceinline__ float exp_scale(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
+}
+
+// eight e2m1 codes times a power of two, exact in bf16
+__device__ __forceinline__ bf16x8 mx4x8_to_bf16(uint32_t c, float s) {
+  u32x4 w;
+  w.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
+  w.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
+  w.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
+  w.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+__device__ __forceinline__ f32x4 mfma_bf16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// U: which byte of the scale words
+template <int U>
+__device__ __forceinline__ f32x4 mfma_mx4(const u32x4& a, const u32x4& b, const f32x4& c, uint32_t sa, uint32_t sb) {
+  const u32x8 A = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  const u32x8 B = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, A), __builtin_bit_cast(i32x8, B), c,
+                                                          4, 4, U, (int)sa, U, (int)sb);
+}
+
+__device__ __forceinline__ void put_y(const ExpertsArgs& a, int64_t m, int64_t n, float y) {
+  if (a.ydtype == DT_F32) ((float*)a.Y)[m * a.ldy + n] = y;
+  else ((uint16_t*)a.Y)[m * a.ldy + n] = (uint16_t)bf16_rne(y);
+}
+
+// Writes one 16x16 tile's four sums of this lane: rows n .. n + 3 of the
+// packed weights at grouped row m.
+__device__ __forceinline__ void put_tile(const ExpertsDesc& d, const ExpertsArgs& a, int64_t m, int64_t n,
+                                         const f32x4& v) {
+  if (d.glu) {
+    const int64_t I = d.N / 2, i = n / 2;
+    const float y0 = v[0] / (1.0f + __expf(-v[0])) * v[1], y1 = v[2] / (1.0f + __expf(-v[2])) * v[3];
+    if (a.yvec && i + 1 < I) {
+      if (a.ydtype == DT_F32) *(float2*)((float*)a.Y + m * a.ldy + i) = float2{y0, y1};
+      else *(uint32_t*)((uint16_t*)a.Y + m * a.ldy + i) = bf16_rne(y0) | (bf16_rne(y1) << 16);
+    } else {
+      if (i < I) put_y(a, m, i, y0);
+      if (i + 1 < I) put_y(a, m, i + 1, y1);
+    }
+  } else if (a.yvec && n + 3 < d.N) {
+    if (a.ydtype == DT_F32) {
+      *(f32x4*)((float*)a.Y + m * a.ldy + n) = v;
+    } else {
+      uint2 w;
+      w.x = bf16_rne(v[0]) | (bf16_rne(v[1]) << 16);
+      w.y = bf16_rne(v[2]) | (bf16_rne(v[3]) << 16);
+      *(uint2*)((uint16_t*)a.Y + m * a.ldy + n) = w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < d.N) put_y(a, m, n + q, v[q]);
+  }
+}
+
+// WK: bf16 (false) or mx4 (true) weights; XK: the same of the activations
+template <bool WK, bool XK, int NW, int R, int T, int C, int D, int WPS>
+__global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, ExpertsArgs a, ExpertsPlan p) {
+  static_assert(WK || !XK, "mx4 activations take mx4 weights");
+  static_assert(D <= C || T >= 4, "the wait for a buffer's copies leaves C stages of weights in flight");
+  constexpr int kRows = 16 * T;
+  constexpr uint32_t kStage = kRows * kStageBytes;       // a stage's rows in LDS
+  constexpr uint32_t kScales = XK ? kRows * 16u : 0u;    // and their exponent bytes
+  constexpr uint32_t kBuf = C * (kStage + kScales);
+  constexpr int NL = WK && !XK ? 1 : 4;                  // 16-byte weight loads per row tile and stage
+  constexpr int kLoads = R * (NL + (WK ? 1 : 0));        // weight loads per wave and stage
+  constexpr int kWait = C * kLoads;
+  static_assert(kWait < 64, "the wait fits the counter");
+  constexpr int U = 2 * C > D ? 2 * C : D;               // stages per pass of the unrolled loop
+  __shared__ __attribute__((aligned(1024))) uint8_t xb0[kBuf];
+  __shared__ __attribute__((aligned(1024))) uint8_t xb1[kBuf];
+  __shared__ int last_flag;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4;
+
+  // ---- which tile ----
+  const int S = p.splits;
+  int s, rg, j;
+  {
+    LinearPlan q{};
+    q.splits = S;
+    q.rgroups = p.rgroups;
+    q.mgroups = p.mgroups;
+    q.rblock = p.rblock;
+    q.xcd_remap = gridDim.x % 8 == 0;
+    tile_coords(blockIdx.x, gridDim.x, q, s, rg, j);
+  }
+  int e, cnt;
+  int64_t row0;
+  find_group(d, a, kRows, j, e, row0, cnt);
+  e = __builtin_amdgcn_readfirstlane(e);
+  cnt = __builtin_amdgcn_readfirstlane(cnt);
+  row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)row0);
+  if (cnt <= 0) return;
+  const int nst = (int)(XK ? (d.NU + 3) / 4 : d.NU);  // stages of K
+  int lo, hi;
+  split_range(nst, s, S, lo, hi);
+  const int n = hi - lo;
+
+  // ---- weights: this wave's row tiles (those past the last read zeros) ----
+  const int64_t rt0 = (int64_t)rg * (NW * R) + wave * R;
+  const int64_t nrt = d.NT - rt0 <= 0 ? 0 : d.NT - rt0 < R ? d.NT - rt0 : R;
+  const __amdgpu_buffer_rsrc_t wr =
+      make_rsrc(d.wpack + ((int64_t)e * d.NT + (nrt ? rt0 : 0)) * d.tile_bytes, (uint32_t)(nrt * d.tile_bytes));
+  const uint32_t tb = (uint32_t)d.tile_bytes, so = (uint32_t)d.scale_off;
+  u32x4 w[D][R][NL];
+  uint32_t sc[D][WK ? R : 1];
+  auto load_w = [&](auto slot, int r, int i, int c) __attribute__((always_inline)) {
+    const int st = lo + c;
+    uint32_t off = (uint32_t)r * tb;
+    bool in = c < n;
+    if constexpr (!WK) off += (uint32_t)st * 4096u + 1024u * i;
+    else if constexpr (!XK) off += (uint32_t)st * 1024u;
+    else {
+      off += (uint32_t)(4 * st + i) * 1024u;
+      in = in && 4 * st + i < (int)d.NU;
+    }
+    w[decltype(slot)::value][r][i] = buf_load16(wr, 16 * lane, in ? off : kOutOfRange);
+  };
+  auto load_s = [&](auto slot, int r, int c) __attribute__((always_inline)) {
+    if constexpr (WK) {
+      const int st = lo + c;
+      const uint32_t off = (uint32_t)r * tb + so + (uint32_t)(XK ? st : st >> 2) * 256u;
+      sc[decltype(slot)::value][r] = buf_load4(wr, 4 * lane, c < n ? off : kOutOfRange);
+    }
+  };
+
+  // ---- activations.  A copy takes four rows x 256 bytes: lane l row l / 16,
+  // piece (l % 16) ^ (row % 8) of 16 bytes, so that the lanes reading one
+  // piece of eight rows hit different banks.  Rows past the group and bytes
+  // past the row take an offset beyond the resource and land as zeros. ----
+  constexpr int kQ = 4 * T;                           // copies of a stage
+  constexpr int kPer = C * kQ / NW;                   // copies of a buffer per wave
+  constexpr int kRowsPer = kQ >= NW ? kQ / NW : 1;    // different rows among them
+  static_assert(C * kQ % NW == 0 && (kQ % NW == 0 || NW % kQ == 0), "every wave copies the same share");
+  const int64_t xrow0 = a.rows ? 0 : row0;
+  const int64_t xrows = a.rows ? a.M : cnt;
+  const i32x4 xr = rsrc_words(a.X + xrow0 * a.ldx, (uint32_t)((xrows - 1) * a.ldx + a.xbytes));
+  auto x_row = [&](int local) -> uint32_t {  // row of X behind row `local` of the group, or out of range
+    if (local >= cnt) return 0xFFFFFFFFu;
+    if (!a.rows) return (uint32_t)local;
+    const int64_t q = a.rows[row0 + local];
+    return q < 0 || q >= a.M ? 0xFFFFFFFFu : (uint32_t)q;
+  };
+  const int q0 = kQ >= NW ? wave : wave % kQ;
+  const int cr = lane >> 4, piece = (lane & 15) ^ ((4 * (q0 & 1) + cr) & 7);
+  uint32_t xo[kRowsPer];
+#pragma unroll
+  for (int i = 0; i < kRowsPer; ++i) {
+    const uint32_t r = x_row(4 * (q0 + NW * i) + cr);
+    xo[i] = r == 0xFFFFFFFFu ? kOutOfRange : r * (uint32_t)a.ldx + 16u * piece;
+  }
+  // exponent bytes of mx4 activations: a copy takes 16 rows x 16 bytes
+  constexpr int kSPer = XK ? (C * T + NW - 1) / NW : 1;
+  uint32_t xso[kSPer];
+  i32x4 xsr{};
+  if constexpr (XK) {
+    xsr = rsrc_words(a.xs + xrow0 * a.ldxs, (uint32_t)(xrows * a.ldxs));
+#pragma unroll
+    for (int i = 0; i < kSPer; ++i) {
+      const uint32_t r = x_row(16 * ((wave + NW * i) % T) + (lane >> 2));
+      xso[i] = r == 0xFFFFFFFFu ? kOutOfRange : r * (uint32_t)a.ldxs + 4u * (lane & 3);
+    }
+  }
+  // buffer m: stages C m .. C m + C - 1 of this split
+  auto copy_x = [&](int m, uint8_t* buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int q = kQ >= NW ? wave + NW * (i % kRowsPer) : q0;
+      const int st = kQ >= NW ? i / kRowsPer : wave / kQ + i * (NW / kQ);
+      const int at = lo + m * C + st;  // stage of K
+      const int left = (int)a.xbytes - at * kStageBytes;
+      const uint32_t v = 16 * piece >= left || at >= hi ? kOutOfRange : xo[i % kRowsPer];
+      copy16<false>(xr, lds_addr(buf) + st * kStage + q * 1024u, v, (uint32_t)(at < hi ? at * kStageBytes : 0));
+    }
+    if constexpr (XK) {
+#pragma unroll
+      for (int i = 0; i < kSPer; ++i) {
+        const int id = wave + NW * i, st = id / T, at = lo + m * C + st;
+        if (id < C * T)
+          copy4<false>(xsr, lds_addr(buf) + C * kStage + id * 256u, at >= hi ? kOutOfRange : xso[i],
+                       (uint32_t)(at < hi ? at * 16 : 0));
+      }
+    }
+  };
+
+  // this lane's piece of row lane % 16 for step i
+  const int fr = lane & 15;
+  auto frag_off = [&](int i) __attribute__((always_inline)) -> uint32_t {
+    const int pc = WK && !XK ? 4 * g + i : 4 * i + g;
+    return (uint32_t)(fr * kStageBytes + 16 * (pc ^ (fr & 7)));
+  };
+  uint32_t fo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fo[i] = frag_off(i);
+
+  f32x4 acc[R][T];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  copy_x(0, xb0);
+  static_for<0, D>([&](auto sl) __attribute__((always_inline)) {
+    constexpr int c = decltype(sl)::value;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      load_s(sl, r, c);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) load_w(sl, r, i, c);
+    }
+  });
+  // the copies are older than the D stages of weights
+  constexpr int kFirst = D * kLoads;
+  __builtin_amdgcn_s_waitcnt((int)((kFirst & 15) | ((kFirst >> 4) << 14) | (7 << 4) | (0 << 8)));
+  barrier_no_fence();
+
+  for (int c0 = 0; c0 < n; c0 += U) {
+    bool done = false;
+    static_for<0, U>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      constexpr int slot = i % D, buf = (i / C) & 1, at = i % C;
+      const int c = c0 + i;
+      if (done || c >= n) {
+        done = true;
+        return;
+      }
+      if constexpr (at == 0) {
+        if (c + C < n) copy_x((c0 + i) / C + 1, buf ? xb0 : xb1);
+      }
+      const uint8_t* xs = (buf ? xb1 : xb0) + at * kStage;
+      const uint8_t* xe = (buf ? xb1 : xb0) + C * kStage + at * kScales;
+      uint32_t sb[XK ? T : 1];
+      if constexpr (XK) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) sb[t] = *(const uint32_t*)(xe + t * 256 + fr * 16 + 4 * g);
+      }
+      float wsc[WK && !XK ? R : 1];
+      if constexpr (WK && !XK) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) wsc[r] = exp_scale((sc[slot][r] >> (8 * ((lo + c) & 3))) & 255u);
+      }
+      static_for<0, 4>([&](auto jc) __attribute__((always_inline)) {
+        constexpr int q = decltype(jc)::value;
+        bf16x8 A[R];
+        if constexpr (!XK) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if constexpr (WK) A[r] = mx4x8_to_bf16(w[slot][r][0][q], wsc[r]);
+            else A[r] = as_bf16x8(w[slot][r][q]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const u32x4 b = *(const u32x4*)(xs + t * (16 * kStageBytes) + fo[q]);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if constexpr (XK) acc[r][t] = mfma_mx4<q>(w[slot][r][q], b, acc[r][t], sc[slot][r], sb[t]);
+            else acc[r][t] = mfma_bf16(A[r], as_bf16x8(b), acc[r][t]);
+          }
+        }
+        // refill what this step was the last to read
+        if constexpr (NL == 4) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) load_w(std::integral_constant<int, slot>{}, r, q, c + D);
+        }
+        if constexpr (q == 3) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if constexpr (NL == 1) load_w(std::integral_constant<int, slot>{}, r, 0, c + D);
+            load_s(std::integral_constant<int, slot>{}, r, c + D);
+          }
+        }
+      });
+      if constexpr (at == C - 1) {
+        // the other buffer's copies have landed (the weights loaded since stay
+        // in flight) and this buffer's reads are done
+        __builtin_amdgcn_s_waitcnt((int)((kWait & 15) | ((kWait >> 4) << 14) | (7 << 4) | (0 << 8)));
+        barrier_no_fence();
+      }
+    });
+  }
+  SPENSE_WAIT_VM(0);
+
+  // ---- epilogue: lane l holds sums of packed rows 4 (l / 16) + 0..3 of a row
+  // tile at activation row l % 16 of an m-tile ----
+  const int nb = 4 * g;
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws, S > 1 ? (uint32_t)((int64_t)S * d.NT * a.R * 64) : 0u);
+  auto poff = [&](int64_t split, int64_t rt, int64_t m) {
+    return (uint32_t)((((split * d.NT + rt) * a.R + m) * 16 + nb) * 4);
+  };
+  if (S > 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        if (rt0 + r < d.NT && 16 * t + fr < cnt) store_partial(wsr, poff(s, rt0 + r, row0 + 16 * t + fr), acc[r][t]);
+    if (!arrive_last(a.counters + (int64_t)j * p.rgroups + rg, S, &last_flag)) return;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (rt0 + r >= d.NT) break;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      if (16 * t + fr >= cnt) continue;
+      const int64_t m = row0 + 16 * t + fr;
+      f32x4 v = acc[r][t];
+      if (S > 1) {
+        // in split order, eight at a time (one memory round trip per eight)
+        v = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int s0 = 0; s0 < S; s0 += 8) {
+          f32x4 part[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) part[q] = load_partial(wsr, s0 + q < S ? poff(s0 + q, rt0 + r, m) : kOutOfRange);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (s0 + q < S) v += part[q];
+        }
+      }
+      put_tile(d, a, m, (rt0 + r) * 16 + nb, v);
+    }
+  }
+}
+
+template <bool WK, bool XK, int NW, int R, int T, int C, int D, int WPS>
+hipError_t launch_k(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPlan& p, hipStream_t s) {
+  if (p.rgroups != (d.NT + NW * R - 1) / (NW * R)) return hipErrorInvalidValue;
+  const int64_t grid = (int64_t)p.rgroups * p.mgroups * p.splits;
+  if (grid < 1 || grid * NW * 64 > 0x7FFFFFFF) return hipErrorInvalidValue;  // threads count in 32 bits
+  experts_kernel<WK, XK, NW, R, T, C, D, WPS><<<(unsigned)grid, NW * 64, 0, s>>>(d, a, p);
+  return hipGetLastError();
+}
+
+template <bool WK, bool XK>
+hipError_t launch_t(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPlan& p, hipStream_t s) {
+  switch (p.config) {
+#define SPENSE_EXPERT_CASE(i, nw, r, t, c, dd, wps) \
+  case i: return launch_k<WK, XK, nw, r, t, c, dd, wps>(d, a, p, s);
+    SPENSE_EXPERT_CONFIGS(SPENSE_EXPERT_CASE)
+#undef SPENSE_EXPERT_CASE
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// Rows of bf16 into rows of ldo bytes, columns from K on zero; eight columns a thread.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
+                                                       const int32_t* rows, int64_t R, uint8_t* out, int64_t ldo) {
+  const int64_t per = ldo / 16, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= R * per) return;
+  const int64_t r = id / per, k = (id - r * per) * 8;
+  const int64_t src = rows ? rows[r] : r;
+  uint16_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = src >= 0 && src < M && k + i < K ? X[src * ldx + k + i] : (uint16_t)0;
+  u32x4 o;
+  o.x = v[0] | ((uint32_t)v[1] << 16);
+  o.y = v[2] | ((uint32_t)v[3] << 16);
+  o.z = v[4] | ((uint32_t)v[5] << 16);
+  o.w = v[6] | ((uint32_t)v[7] << 16);
+  *(u32x4*)(out + r * ldo + 2 * k) = o;
+}
+
+}  // namespace
+
+int experts_config_count() {
+  int n = 0;
+#define SPENSE_EXPERT_COUNT(i, nw, r, t, c, dd, wps) ++n;
+  SPENSE_EXPERT_CONFIGS(SPENSE_EXPERT_COUNT)
+#undef SPENSE_EXPERT_COUNT
+  return n;
+}
+
+ExpertsShape experts_shape(int config) {
+  switch (config) {
+#define SPENSE_EXPERT_SHAPE(i, nw, r, t, c, dd, wps) \
+  case i: return ExpertsShape{nw, r, t};
+    SPENSE_EXPERT_CONFIGS(SPENSE_EXPERT_SHAPE)
+#undef SPENSE_EXPERT_SHAPE
+    default: return ExpertsShape{0, 0, 0};
+  }
+}
+
+hipError_t launch_experts(const ExpertsDesc& d, const ExpertsArgs& a, int32_t xdtype, const ExpertsPlan& p,
+                          hipStream_t s) {
+  if (d.wdtype == DT_BF16) return xdtype == DT_BF16 ? launch_t<false, false>(d, a, p, s) : hipErrorInvalidValue;
+  return xdtype == DT_MX4 ? launch_t<true, true>(d, a, p, s) : launch_t<true, false>(d, a, p, s);
+}
+
+hipError_t launch_pad_rows(const void* X, int64_t M, int64_t K, int64_t ldx, const int32_t* rows, int64_t R, void* out,
+                           int64_t ldo, hipStream_t s) {
+  // a launch's grid counts threads in 32 bits: runs of rows of at most 2^30
+  const int64_t per = ldo / 16, most = (int64_t(1) << 30) / per;
+  for (int64_t r = 0; r < R; r += most) {
+    const int64_t n = R - r < most ? R - r : most;
+    pad_rows_kernel<<<(unsigned)((n * per + 255) / 256), 256, 0, s>>>(
+        (const uint16_t*)X + (rows ? 0 : r * ldx), rows ? M : n, K, ldx, rows ? rows + r : nullptr, n,
+        (uint8_t*)out + r * ldo, ldo);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace spense

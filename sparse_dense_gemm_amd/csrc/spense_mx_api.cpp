@@ -1,0 +1,245 @@
+// Host side of the mx4 and experts' layers: packing, launch planning,
+// workspaces.  Arguments have been checked by the entry points in
+// spense_api.cpp.
+#include <algorithm>
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+
+#include "../../include/spense.h"
+#include "spense_mx.h"
+
+namespace spense {
+
+struct ExpertsLayer {
+  ExpertsDesc d{};
+  int64_t weight_bytes = 0;
+  int64_t device_bytes = 0;
+  // workspaces, shared by the calls on the handle (one in flight)
+  uint8_t* xws = nullptr;  // activations laid out for the product kernel
+  size_t xws_bytes = 0;
+  float* ws = nullptr;     // partial sums
+  size_t ws_bytes = 0;
+  int32_t* counters = nullptr;
+  size_t n_counters = 0;
+};
+
+namespace {
+
+constexpr int64_t kMaxPartials = int64_t(64) << 20;  // bytes of partial sums a plan may ask for
+constexpr int kCUs = 256;
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+int status_of(hipError_t e) {
+  const int rc = report_hip(e);
+  return e == hipErrorOutOfMemory ? SPENSE_ENOMEM : rc;
+}
+
+// Launch plan of R grouped rows (a function of ceil(R / 16) only, so that the
+// workspaces of every smaller call can be sized by stepping over it).
+ExpertsPlan make_plan(const ExpertsDesc& d, bool grouped, int64_t R, bool xmx) {
+  const int64_t R16 = (R + 15) / 16 * 16;
+  const int64_t hit = grouped ? std::min(d.E, R16) : 1;  // experts that may have rows
+  const int64_t rows = (R16 + hit - 1) / hit;            // rows of one, on average
+  ExpertsPlan p{};
+  int f_config = -1, f_splits = 0, f_rblock = 0;  // forced by SPENSE_EXPERTS=config[,splits[,rblock]] (tests, tuning)
+  if (const char* v = getenv("SPENSE_EXPERTS")) {
+    sscanf(v, "%d,%d,%d", &f_config, &f_splits, &f_rblock);
+    if (f_config >= experts_config_count()) f_config = -1;
+  }
+  // the smallest m-tile count that takes an average expert's rows in one group
+  p.config = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 3 : 4;
+  if (f_config >= 0) p.config = f_config;
+  const ExpertsShape c = experts_shape(p.config);
+  const int64_t per = c.waves * c.r, take = 16 * c.t;
+  p.rgroups = (int)((d.NT + per - 1) / per);
+  // sum over experts of ceil(n / take) for any split of R rows over `hit` experts
+  p.mgroups = (int)(grouped ? (R16 - hit) / take + hit : (R16 + take - 1) / take);
+  // split K where the tiles alone leave CUs without a workgroup
+  const int64_t stages = xmx ? (d.NU + 3) / 4 : d.NU;
+  const int64_t tiles = (int64_t)p.rgroups * p.mgroups;
+  const int64_t want = c.t <= 4 ? 2 * kCUs : kCUs;
+  int64_t S = tiles >= want ? 1 : (want + tiles / 2) / tiles;
+  S = std::min<int64_t>({S, std::max<int64_t>(1, stages / (xmx ? 2 : 4)), 64});
+  if (f_splits > 0) S = std::min<int64_t>(f_splits, std::min<int64_t>(stages, 64));
+  while (S > 1 && S * d.NT * R16 * 64 > kMaxPartials) --S;
+  p.splits = (int)S;
+  p.rblock = c.t >= 8 && p.mgroups > 1 ? 8 : 1;
+  if (f_rblock > 0) p.rblock = f_rblock;
+  return p;
+}
+
+struct Need {
+  int64_t xws = 0, ws = 0, cnt = 0;
+  void grow(const Need& o) {
+    xws = std::max(xws, o.xws);
+    ws = std::max(ws, o.ws);
+    cnt = std::max(cnt, o.cnt);
+  }
+};
+
+Need plan_need(const ExpertsDesc& d, const ExpertsPlan& p, int64_t R) {
+  Need n;
+  if (p.splits > 1) {
+    n.ws = (int64_t)p.splits * d.NT * ((R + 15) / 16 * 16) * 64;
+    n.cnt = (int64_t)p.rgroups * p.mgroups;
+  }
+  return n;
+}
+
+bool fits(const ExpertsLayer* h, const Need& n) {
+  return (int64_t)h->xws_bytes >= n.xws && (int64_t)h->ws_bytes >= n.ws && (int64_t)h->n_counters >= n.cnt;
+}
+
+// Replaces the workspaces that are too small (earlier launches may still use
+// them, so the stream is synchronised first).
+int grow(ExpertsLayer* h, const Need& n, hipStream_t s) {
+  hipError_t e = hipStreamSynchronize(s);
+  if (e != hipSuccess) return status_of(e);
+  auto regrow = [&](void** p, size_t& have, int64_t want) -> int {
+    if (want <= (int64_t)have) return SPENSE_OK;
+    if (*p) (void)hipFree(*p);
+    *p = nullptr;
+    have = 0;
+    const hipError_t err = hipMalloc(p, (size_t)want);
+    if (err != hipSuccess) return status_of(err);
+    have = (size_t)want;
+    return SPENSE_OK;
+  };
+  int rc = regrow((void**)&h->xws, h->xws_bytes, n.xws);
+  if (rc == SPENSE_OK) rc = regrow((void**)&h->ws, h->ws_bytes, n.ws);
+  if (rc == SPENSE_OK && n.cnt > (int64_t)h->n_counters) {
+    size_t bytes = h->n_counters * 4;
+    rc = regrow((void**)&h->counters, bytes, n.cnt * 4);
+    h->n_counters = bytes / 4;
+    if (rc == SPENSE_OK) {
+      e = launch_zero_i32(h->counters, n.cnt, s);
+      if (e != hipSuccess) rc = status_of(e);
+    }
+  }
+  return rc;
+}
+
+}  // namespace
+
+void experts_release(ExpertsLayer* h) {
+  if (!h) return;
+  void* ptrs[] = {h->d.wpack, h->xws, h->ws, h->counters};
+  for (void* p : ptrs)
+    if (p) (void)hipFree(p);
+  delete h;
+}
+
+int experts_pack(const void* W, int32_t wdtype, const uint8_t* scales, int64_t E, int64_t N, int64_t K, int64_t ldw,
+                 int64_t lds, int32_t glu, hipStream_t s, ExpertsLayer** out) {
+  ExpertsLayer* h = new (std::nothrow) ExpertsLayer();
+  if (!h) return SPENSE_ENOMEM;
+  ExpertsDesc& d = h->d;
+  const bool mx = wdtype == SPENSE_MX4;
+  d.E = E;
+  d.N = N;
+  d.K = K;
+  d.wdtype = wdtype;
+  d.glu = glu ? 1 : 0;
+  d.NT = (N + kRowTile - 1) / kRowTile;
+  d.NU = mx_units(K);
+  d.scale_off = mx ? d.NU * 1024 : 0;
+  d.tile_bytes = mx ? d.scale_off + (d.NU + 3) / 4 * 256 : d.NU * 4096;
+  h->weight_bytes = mx ? E * N * ((K + 1) / 2 + (K + kMxBlock - 1) / kMxBlock) : E * N * K * 2;
+  h->device_bytes = E * d.NT * d.tile_bytes;
+  hipError_t e = hipMalloc((void**)&d.wpack, (size_t)h->device_bytes);
+  if (e != hipSuccess) d.wpack = nullptr;
+  if (e == hipSuccess) e = launch_pack_experts(d, W, ldw, scales, lds, s);
+  if (e == hipSuccess) e = hipStreamSynchronize(s);
+  if (e != hipSuccess) {
+    (void)hipStreamSynchronize(s);
+    experts_release(h);
+    return status_of(e);
+  }
+  *out = h;
+  return SPENSE_OK;
+}
+
+void experts_info(const ExpertsLayer* h, spense_layer_info* info) {
+  info->N = h->d.N;
+  info->K = h->d.K;
+  info->K_d = h->d.K;
+  info->wdtype = h->d.wdtype;
+  info->weight_bytes = h->weight_bytes;
+  info->device_bytes = h->device_bytes;
+  info->N_s = h->d.E;
+  info->N_d = h->d.glu ? h->d.N / 2 : h->d.N;
+}
+
+const ExpertsDesc& experts_desc(const ExpertsLayer* h) { return h->d; }
+
+int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64_t ldx, const int32_t* rows,
+                const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, hipStream_t s) {
+  const ExpertsDesc& d = h->d;
+  const bool xmx = adtype == SPENSE_MX4;
+  const ExpertsPlan p = make_plan(d, offsets != nullptr, R, xmx);
+  ExpertsArgs a{};
+  a.rows = rows;
+  a.offsets = offsets;
+  a.R = R;
+  a.Y = Y;
+  a.ldy = ldy;
+  a.ydtype = ydtype;
+  a.yvec = ((uintptr_t)Y & 15) == 0 && ldy % 4 == 0;
+  // The product kernel reads rows of 16-byte pieces through offsets of 31
+  // bits: mx4 activations are quantised into that form, bf16 ones are read in
+  // place if they have it and laid out first if not.  Rows picked from beyond
+  // 31 bits are gathered by the same pass.
+  constexpr int64_t kSpan = int64_t(1) << 31;
+  Need need = plan_need(d, p, R);
+  int64_t codes_bytes = 0, n_rows = M;
+  bool prepare = true;
+  if (xmx) {
+    a.ldx = d.NU * 64;
+    a.ldxs = (d.NU + 3) / 4 * 16;
+    a.xbytes = a.ldx;
+    if (rows && M * a.ldx >= kSpan) n_rows = R;
+    codes_bytes = align256(n_rows * a.ldx);
+    need.xws = codes_bytes + n_rows * a.ldxs;
+  } else {
+    prepare = ((uintptr_t)X & 15) != 0 || ldx % 8 != 0 || d.K % 8 != 0 || 2 * ldx * 256 >= kSpan ||
+              (rows && 2 * M * ldx >= kSpan);
+    a.ldx = prepare ? (d.K + 7) / 8 * 16 : 2 * ldx;
+    a.xbytes = (d.K + 7) / 8 * 16;
+    if (prepare) {
+      if (rows && M * a.ldx >= kSpan) n_rows = R;
+      need.xws = n_rows * a.ldx;
+    }
+  }
+  if (!fits(h, need)) {
+    for (int64_t r = 16; r < R; r += 16)  // every smaller call too, whichever of its rows it brings
+      need.grow(plan_need(d, make_plan(d, offsets != nullptr, r, xmx), r));
+    const int rc = grow(h, need, s);
+    if (rc != SPENSE_OK) return rc;
+  }
+  hipError_t e = hipSuccess;
+  a.M = M;
+  if (prepare) {
+    const bool gather = n_rows != M || (rows && n_rows == R && M * a.ldx >= kSpan);
+    const int32_t* pick = gather ? rows : nullptr;
+    if (xmx) {
+      a.xs = h->xws + codes_bytes;
+      e = launch_mx4_activations(X, M, d.K, ldx, pick, n_rows, h->xws, a.ldx, h->xws + codes_bytes, a.ldxs, s);
+    } else {
+      e = launch_pad_rows(X, M, d.K, ldx, pick, n_rows, h->xws, a.ldx, s);
+    }
+    if (e != hipSuccess) return status_of(e);
+    a.X = h->xws;
+    a.M = n_rows;
+    if (gather) a.rows = nullptr;
+  } else {
+    a.X = (const uint8_t*)X;
+  }
+  a.ws = h->ws;
+  a.counters = h->counters;
+  e = launch_experts(d, a, xmx ? DT_MX4 : DT_BF16, p, s);
+  return e == hipSuccess ? SPENSE_OK : status_of(e);
+}
+
+}  // namespace spense

@@ -1,0 +1,352 @@
+// HIP kernels of the expert router and of the weighted sum over a token's
+// experts.
+//
+// Route: each token takes the k experts with the largest logits (NaN and -inf
+// logits are never taken, equal ones go to the lower expert) with softmax
+// weights, and the (token, choice) pairs are grouped by expert, in token order
+// within an expert.  A token takes an expert at most once, so a bit per token
+// and expert says everything about a block of tokens: an expert's rows in the
+// block are the set bits, a token's place among them the set bits below its
+// own.  The bits are set by LDS atomics whose order does not matter, so the
+// result does not depend on it.  One launch for a single block of tokens, else
+// two: the first leaves each block's counts in the workspace, the second adds
+// up the counts of the blocks before its own.
+#include "spense_device.h"
+#include "spense_mx.h"
+
+namespace spense {
+namespace {
+
+// order-preserving bits of a logit; 0 for one that is never taken
+__device__ __forceinline__ uint32_t logit_key(float l) {
+  if (!(l > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(l + 0.0f);  // -0 becomes +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+__device__ __forceinline__ float load_logit(const void* p, int32_t type, int64_t i) {
+  return type == DT_F32 ? ((const float*)p)[i] : __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+}
+
+// exp(l - max), also where both are +inf
+__device__ __forceinline__ float weight_of(float l, float top) { return l == top ? 1.0f : expf(l - top); }
+
+// Inclusive scan over the workgroup's threads (a multiple of 64 of them, at
+// most 1024); tmp: 16 ints of LDS.
+__device__ __forceinline__ int block_scan(int v, int* tmp) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(v, o);
+    if (lane >= o) v += up;
+  }
+  if (lane == 63) tmp[wave] = v;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < wave; ++i) before += tmp[i];
+  __syncthreads();
+  return v + before;
+}
+
+// The choices of TB tokens.  G lanes share a token, V logits each.  With one
+// block of tokens (fused) it also writes offsets, rows and final places;
+// otherwise the block's counts and each choice's place within the block.
+template <int G, int V>
+__global__ __launch_bounds__(256) void choose_kernel(RouteArgs a, int TB, int fused) {
+  extern __shared__ uint32_t bits[];  // [E][TB / 32], then (fused) [E] first rows
+  __shared__ int tmp[16], last;
+  const int words = TB / 32;
+  const int E = (int)a.E;
+  for (int i = threadIdx.x; i < E * words; i += 256) bits[i] = 0u;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * TB;
+  const int sub = threadIdx.x % G;
+  constexpr int kTokens = 256 / G;  // tokens at a time
+  for (int tb = 0; tb < TB; tb += kTokens) {
+    const int tl = tb + threadIdx.x / G;
+    const int64_t t = t0 + tl;
+    const bool in = t < a.T;
+    uint32_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = sub + G * v;
+      key[v] = in && e < E ? logit_key(load_logit(a.logits, a.ltype, t * a.ldl + e)) : 0u;
+    }
+    // softmax over every expert that may be taken, if the weights are not
+    // renormalised over the chosen ones
+    float total = 0.f, top = 0.f;
+    if (!a.renormalize) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) m = key[v] > m ? key[v] : m;
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1) {
+        const uint32_t x = (uint32_t)__shfl_xor((int)m, o, G);
+        m = x > m ? x : m;
+      }
+      top = key_logit(m);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (key[v]) total += weight_of(key_logit(key[v]), top);
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1) total += __shfl_xor(total, o, G);
+    }
+    float chosen = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t m = 0;
+      int e = 0;
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v)
+        if (key[v] >= m) {  // equal keys: the lower expert
+          m = key[v];
+          e = sub + G * v;
+        }
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1) {
+        const uint32_t m2 = (uint32_t)__shfl_xor((int)m, o, G);
+        const int e2 = __shfl_xor(e, o, G);
+        if (m2 > m || (m2 == m && e2 < e)) {
+          m = m2;
+          e = e2;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e == sub + G * v) key[v] = 0u;
+      if (a.renormalize && j == 0) top = key_logit(m);
+      const float w = m ? weight_of(key_logit(m), top) : 0.f;
+      chosen += w;
+      if (in && sub == 0) {
+        a.ids[t * a.k + j] = m ? e : -1;
+        a.weights[t * a.k + j] = w;
+        if (m) atomicOr(&bits[e * words + (tl >> 5)], 1u << (tl & 31));
+      }
+    }
+    const float sum = a.renormalize ? chosen : total;
+    if (in && sub == 0 && sum > 0.f)
+      for (int j = 0; j < a.k; ++j) a.weights[t * a.k + j] /= sum;
+  }
+  __syncthreads();
+  // counts, and (fused) the experts' first rows
+  int* first = (int*)(bits + E * words);
+  int carry = 0;
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    const int e = e0 + threadIdx.x;
+    int n = 0;
+    if (e < E)
+      for (int i = 0; i < words; ++i) n += __popc(bits[e * words + i]);
+    if (!fused) {
+      if (e < E) a.work[(int64_t)blockIdx.x * E + e] = n;
+    } else {
+      const int incl = block_scan(n, tmp) + carry;
+      if (e < E) {
+        first[e] = incl - n;
+        a.offsets[e] = incl - n;
+        if (e == E - 1) a.offsets[E] = incl;
+      }
+      if (threadIdx.x == 255) last = incl;
+      __syncthreads();
+      carry = last;
+      __syncthreads();
+    }
+  }
+  const int64_t left = a.T - t0;
+  const int pairs = (int)((left < TB ? left : TB) * a.k);
+  for (int i = threadIdx.x; i < pairs; i += 256) {
+    const int tl = i / a.k;
+    const int64_t at = t0 * a.k + i;
+    const int e = a.ids[at];
+    int place = -1;
+    if (e >= 0) {
+      place = __popc(bits[e * words + (tl >> 5)] & ((1u << (tl & 31)) - 1u));
+      for (int q = 0; q < (tl >> 5); ++q) place += __popc(bits[e * words + q]);
+      if (fused) {
+        place += first[e];
+        a.rows[place] = (int)(t0 + tl);
+      }
+    }
+    a.pos[at] = place;
+  }
+  if (fused)
+    for (int64_t r = carry + threadIdx.x; r < a.T * a.k; r += 256) a.rows[r] = -1;
+}
+
+// Places of one block's choices: the counts of all blocks give the experts'
+// first rows, those of the blocks before this one its own start among them.
+__global__ __launch_bounds__(256) void place_kernel(RouteArgs a, int TB, int blocks) {
+  extern __shared__ int base[];  // [E]
+  __shared__ int tmp[16], last;
+  const int E = (int)a.E;
+  const int b = blockIdx.x;
+  int carry = 0;
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    const int e = e0 + threadIdx.x;
+    int all = 0, before = 0;
+    if (e < E)
+      for (int i = 0; i < blocks; ++i) {
+        const int n = a.work[(int64_t)i * E + e];
+        all += n;
+        before += i < b ? n : 0;
+      }
+    const int incl = block_scan(all, tmp) + carry;
+    if (e < E) {
+      base[e] = incl - all + before;
+      if (b == 0) {
+        a.offsets[e] = incl - all;
+        if (e == E - 1) a.offsets[E] = incl;
+      }
+    }
+    if (threadIdx.x == 255) last = incl;
+    __syncthreads();
+    carry = last;
+    __syncthreads();
+  }
+  const int64_t t0 = (int64_t)b * TB, left = a.T - t0;
+  const int pairs = (int)((left < TB ? left : TB) * a.k);
+  for (int i = threadIdx.x; i < pairs; i += 256) {
+    const int64_t at = t0 * a.k + i;
+    const int e = a.ids[at];
+    if (e < 0) continue;
+    const int place = a.pos[at] + base[e];
+    a.pos[at] = place;
+    a.rows[place] = (int)(t0 + i / a.k);
+  }
+  // rows past the last choice
+  for (int i = threadIdx.x; i < pairs; i += 256) {
+    const int64_t r = t0 * a.k + i;
+    if (r >= carry) a.rows[r] = -1;
+  }
+}
+
+// Y[t, n .. n + 3] = sum_j weights[t, j] O[pos[t, j], n .. n + 3], in the order of j
+template <typename OT>
+__global__ __launch_bounds__(256) void combine_kernel(const OT* O, int64_t R, int64_t ldo, const int32_t* pos,
+                                                      const float* weights, int64_t T, int64_t k, int64_t N, void* Y,
+                                                      int32_t ydtype, int64_t ldy, bool vec) {
+  const int64_t per = (N + 3) / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = id / per, n = (id - t * per) * 4;
+  if (t >= T) return;
+  f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int64_t j = 0; j < k; ++j) {
+    const int64_t r = pos[t * k + j];
+    if (r < 0 || r >= R) continue;
+    const float w = weights[t * k + j];
+    const OT* o = O + r * ldo + n;
+    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+      if constexpr (sizeof(OT) == 4) {
+        v = *(const f32x4*)o;
+      } else {
+        const uint2 u = *(const uint2*)o;
+        v = f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                  __uint_as_float(u.y & 0xFFFF0000u)};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) {
+          if constexpr (sizeof(OT) == 4) v[i] = o[i];
+          else v[i] = __uint_as_float((uint32_t)o[i] << 16);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += w * v[i];
+  }
+  if (ydtype == DT_F32) {
+    float* out = (float*)Y + t * ldy + n;
+    if (vec) *(f32x4*)out = y;
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) out[i] = y[i];
+  } else {
+    uint16_t* out = (uint16_t*)Y + t * ldy + n;
+    if (vec) {
+      uint2 u;
+      u.x = bf16_rne(y[0]) | (bf16_rne(y[1]) << 16);
+      u.y = bf16_rne(y[2]) | (bf16_rne(y[3]) << 16);
+      *(uint2*)out = u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) out[i] = (uint16_t)bf16_rne(y[i]);
+    }
+  }
+}
+
+__global__ void no_rows_kernel(int32_t* offsets, int64_t E) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i <= E) offsets[i] = 0;
+}
+
+// Tokens of a block: 64, more for so many tokens that reading every block's
+// counts (blocks^2 E) would cost more than the tokens do, as far as the bits
+// take 48 KB of LDS.
+int tokens_per_block(int64_t T, int64_t E) {
+  int TB = T <= (int64_t(1) << 14) ? 64 : T <= (int64_t(1) << 17) ? 256 : 1024;
+  while (TB > 64 && E * (TB / 8) > 48 * 1024) TB /= 2;
+  return TB;
+}
+
+template <int G, int V>
+hipError_t choose(const RouteArgs& a, int TB, int blocks, hipStream_t s) {
+  const size_t lds = (size_t)a.E * (TB / 32) * 4 + (blocks == 1 ? (size_t)a.E * 4 : 0);
+  choose_kernel<G, V><<<blocks, 256, lds, s>>>(a, TB, blocks == 1);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t route_work_bytes(int64_t T, int64_t E) {
+  const int TB = tokens_per_block(T, E);
+  const int64_t blocks = (T + TB - 1) / TB;
+  return blocks <= 1 ? 0 : blocks * E * 4;
+}
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  if (a.T == 0) {
+    no_rows_kernel<<<(unsigned)((a.E + 256) / 256), 256, 0, s>>>(a.offsets, a.E);
+    return hipGetLastError();
+  }
+  const int TB = tokens_per_block(a.T, a.E);
+  const int blocks = (int)((a.T + TB - 1) / TB);
+  hipError_t e;
+  if (a.E <= 16) e = choose<16, 1>(a, TB, blocks, s);
+  else if (a.E <= 32) e = choose<16, 2>(a, TB, blocks, s);
+  else if (a.E <= 64) e = choose<16, 4>(a, TB, blocks, s);
+  else if (a.E <= 128) e = choose<16, 8>(a, TB, blocks, s);
+  else if (a.E <= 256) e = choose<16, 16>(a, TB, blocks, s);
+  else if (a.E <= 512) e = choose<64, 8>(a, TB, blocks, s);
+  else e = choose<64, 16>(a, TB, blocks, s);
+  if (e != hipSuccess || blocks == 1) return e;
+  place_kernel<<<blocks, 256, (size_t)a.E * 4, s>>>(a, TB, blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const void* O, int32_t otype, int64_t R, int64_t ldo, const int32_t* pos,
+                          const float* weights, int64_t T, int64_t k, int64_t N, void* Y, int32_t ydtype, int64_t ldy,
+                          hipStream_t s) {
+  const int64_t per = (N + 3) / 4, most = (int64_t(1) << 30) / per;  // a grid counts threads in 32 bits
+  const int ob = otype == DT_F32 ? 4 : 2, yb = ydtype == DT_F32 ? 4 : 2;
+  const bool vec = N % 4 == 0 && ((uintptr_t)O | (uintptr_t)(ldo * ob)) % (4 * ob) == 0 &&
+                   ((uintptr_t)Y | (uintptr_t)(ldy * yb)) % (4 * yb) == 0;
+  for (int64_t t = 0; t < T; t += most) {
+    const int64_t n = T - t < most ? T - t : most;
+    const unsigned grid = (unsigned)((n * per + 255) / 256);
+    void* y = (uint8_t*)Y + t * ldy * yb;
+    if (otype == DT_F32)
+      combine_kernel<float><<<grid, 256, 0, s>>>((const float*)O, R, ldo, pos + t * k, weights + t * k, n, k, N, y,
+                                                 ydtype, ldy, vec);
+    else
+      combine_kernel<uint16_t><<<grid, 256, 0, s>>>((const uint16_t*)O, R, ldo, pos + t * k, weights + t * k, n, k, N,
+                                                    y, ydtype, ldy, vec);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace spense

@@ -52,55 +52,6 @@ namespace {
   X(6, 2, 2, 4, 2, 4)         \
   X(7, 4, 2, 8, 4, 2)
 
-// Buffer descriptor words (the layout make_rsrc builds: base, no stride,
-// num_records bytes, raw-buffer flags), uniform across the wave.
-__device__ __forceinline__ i32x4 rsrc_words(const void* base, uint32_t bytes) {
-  const uint64_t a = (uint64_t)base;
-  i32x4 r;
-  r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF);
-  r.z = __builtin_amdgcn_readfirstlane((int)bytes);
-  r.w = 0x00020000;
-  return r;
-}
-
-// LDS byte address of a pointer into a __shared__ array
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)p;
-}
-
-// Copies into LDS (buffer loads with an LDS destination): lane l's 16 (or 4)
-// bytes at voff + soff of the resource land at LDS address lds + 16 l (4 l);
-// offsets beyond the resource write zeros.  They are written as assembly so
-// that the compiler does not track them: it would otherwise wait for copies
-// into other stage buffers before LDS reads whenever more copies are in
-// flight than it follows one by one.  The kernel waits for them itself (a
-// counted s_waitcnt before each stage's barrier); no other vector-memory
-// load is issued while they are in flight.  NT: non-temporal cache policy.
-template <bool NT>
-__device__ __forceinline__ void copy16(const i32x4& r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  if constexpr (NT)
-    asm volatile("buffer_load_dwordx4 %0, %1, %2 offen nt lds" ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
-  else
-    asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
-}
-template <bool NT>
-__device__ __forceinline__ void copy4(const i32x4& r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  if constexpr (NT)
-    asm volatile("buffer_load_dword %0, %1, %2 offen nt lds" ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
-  else
-    asm volatile("buffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
-}
-
-// f(integral_constant<A>), ..., f(integral_constant<B - 1>), in order
-template <int A, int B, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (A < B) {
-    f(std::integral_constant<int, A>{});
-    static_for<A + 1, B>(f);
-  }
-}
-
 template <typename WT, bool A8, int WR, int WM, int R, int T>
 struct TileShape {
   static constexpr int NWV = WR * WM;                       // waves per workgroup
