@@ -25,15 +25,17 @@ namespace spense {
 namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
-// Configurations: X(index, waves, row tiles per wave R, m-tiles T, stages per
-// LDS buffer C, ring depth D in stages, waves per SIMD the registers allow)
+// Configurations: X(index, waves, row tiles per wave R, m-tiles T, stages D in
+// the ring and in an LDS buffer, waves per SIMD the registers allow)
 #define SPENSE_EXPERT_CONFIGS(X) \
-  X(0, 8, 1, 1, 4, 4, 2)         \
-  X(1, 8, 1, 2, 4, 4, 2)         \
-  X(2, 4, 2, 4, 2, 2, 2)         \
-  X(3, 4, 2, 8, 1, 2, 1)         \
-  X(4, 4, 4, 16, 1, 2, 1)
+  X(0, 8, 1, 1, 4, 2)            \
+  X(1, 8, 1, 2, 4, 2)            \
+  X(2, 4, 2, 4, 2, 2)            \
+  X(3, 4, 2, 8, 1, 2)            \
+  X(4, 4, 4, 8, 1, 2)
 
 // First of the 16 rows and expert of m-tile group j (groups of `rows` rows,
 // counted over the experts in order); cnt = 0 where there is no such group.
@@ -111,57 +113,76 @@ __device__ __forceinline__ f32x4 mfma_mx4(const u32x4& a, const u32x4& b, const 
                                                           4, 4, U, (int)sa, U, (int)sb);
 }
 
-__device__ __forceinline__ void put_y(const ExpertsArgs& a, int64_t m, int64_t n, float y) {
-  if (a.ydtype == DT_F32) ((float*)a.Y)[m * a.ldy + n] = y;
-  else ((uint16_t*)a.Y)[m * a.ldy + n] = (uint16_t)bf16_rne(y);
+// two fp32 as bf16, rounded to nearest even
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  bf16x2 v;
+  v[0] = (__bf16)a;
+  v[1] = (__bf16)b;
+  return __builtin_bit_cast(uint32_t, v);
 }
 
-// Writes one 16x16 tile's four sums of this lane: rows n .. n + 3 of the
-// packed weights at grouped row m.
-__device__ __forceinline__ void put_tile(const ExpertsDesc& d, const ExpertsArgs& a, int64_t m, int64_t n,
-                                         const f32x4& v) {
-  if (d.glu) {
-    const int64_t I = d.N / 2, i = n / 2;
-    const float y0 = v[0] / (1.0f + __expf(-v[0])) * v[1], y1 = v[2] / (1.0f + __expf(-v[2])) * v[3];
-    if (a.yvec && i + 1 < I) {
-      if (a.ydtype == DT_F32) *(float2*)((float*)a.Y + m * a.ldy + i) = float2{y0, y1};
-      else *(uint32_t*)((uint16_t*)a.Y + m * a.ldy + i) = bf16_rne(y0) | (bf16_rne(y1) << 16);
-    } else {
-      if (i < I) put_y(a, m, i, y0);
-      if (i + 1 < I) put_y(a, m, i + 1, y1);
-    }
-  } else if (a.yvec && n + 3 < d.N) {
-    if (a.ydtype == DT_F32) {
-      *(f32x4*)((float*)a.Y + m * a.ldy + n) = v;
-    } else {
-      uint2 w;
-      w.x = bf16_rne(v[0]) | (bf16_rne(v[1]) << 16);
-      w.y = bf16_rne(v[2]) | (bf16_rne(v[3]) << 16);
-      *(uint2*)((uint16_t*)a.Y + m * a.ldy + n) = w;
-    }
-  } else {
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
+// Sixteen activation rows of a wave's R row tiles into Y.  A lane holds four
+// packed rows of each tile (v[r]), four output columns or two gated ones; its
+// own stores would leave 32-byte runs, so the wave turns the block around in
+// its part of LDS and writes each row's columns in runs of 16 bytes per lane.
+// lds: 16 rows of at most 64 R + 16 bytes.  m0: Y row of the first of the
+// `have` rows; col0: output column of the wave's first tile.
+template <int R>
+__device__ __forceinline__ void put_rows(const ExpertsDesc& d, const ExpertsArgs& a, const f32x4 (&v)[R], uint8_t* lds,
+                                         int64_t m0, int have, int64_t col0, bool wide) {
+  const int lane = threadIdx.x & 63, fr = lane & 15, g = lane >> 4;
+  const int eb = a.ydtype == DT_F32 ? 4 : 2;
+  const int cols = d.glu ? 8 * R : 16 * R;           // output columns of the block
+  const int64_t N = d.glu ? d.N / 2 : d.N;
+  const int pitch = cols * eb + 16;
+  uint8_t* row = lds + fr * pitch;
+  asm volatile("" ::: "memory");  // the wave's own LDS accesses stay in this order
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (n + q < d.N) put_y(a, m, n + q, v[q]);
+  for (int r = 0; r < R; ++r) {
+    if (d.glu) {
+      const float y0 = silu_mul(v[r][0], v[r][1]), y1 = silu_mul(v[r][2], v[r][3]);
+      if (eb == 4) *(f32x2*)(row + (8 * r + 2 * g) * 4) = f32x2{y0, y1};
+      else *(uint32_t*)(row + (8 * r + 2 * g) * 2) = bf16_pair(y0, y1);
+    } else {
+      if (eb == 4) *(f32x4*)(row + (16 * r + 4 * g) * 4) = v[r];
+      else *(u32x2*)(row + (16 * r + 4 * g) * 2) = u32x2{bf16_pair(v[r][0], v[r][1]), bf16_pair(v[r][2], v[r][3])};
+    }
+  }
+  asm volatile("" ::: "memory");
+  const int lc = __builtin_ctz(cols * eb / 16);      // 16-byte pieces of a row: a power of two
+  const int per = 16 / eb;
+  for (int i = lane; i < (16 << lc); i += 64) {
+    const int m = i >> lc, c = i & ((1 << lc) - 1);
+    const int64_t col = col0 + c * per;
+    if (m >= have || col >= N) continue;
+    const uint8_t* from = lds + m * pitch + 16 * c;
+    uint8_t* to = (uint8_t*)a.Y + ((m0 + m) * a.ldy + col) * eb;
+    if (wide && col + per <= N) {
+      *(u32x4*)to = *(const u32x4*)from;
+    } else {
+      for (int k = 0; k < per && col + k < N; ++k) {
+        if (eb == 4) ((uint32_t*)to)[k] = ((const uint32_t*)from)[k];
+        else ((uint16_t*)to)[k] = ((const uint16_t*)from)[k];
+      }
+    }
   }
 }
 
 // WK: bf16 (false) or mx4 (true) weights; XK: the same of the activations
-template <bool WK, bool XK, int NW, int R, int T, int C, int D, int WPS>
+template <bool WK, bool XK, int NW, int R, int T, int D, int WPS>
 __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, ExpertsArgs a, ExpertsPlan p) {
   static_assert(WK || !XK, "mx4 activations take mx4 weights");
-  static_assert(D <= C || T >= 4, "the wait for a buffer's copies leaves C stages of weights in flight");
   constexpr int kRows = 16 * T;
   constexpr uint32_t kStage = kRows * kStageBytes;       // a stage's rows in LDS
   constexpr uint32_t kScales = XK ? kRows * 16u : 0u;    // and their exponent bytes
-  constexpr uint32_t kBuf = C * (kStage + kScales);
+  constexpr uint32_t kBuf = D * (kStage + kScales);
   constexpr int NL = WK && !XK ? 1 : 4;                  // 16-byte weight loads per row tile and stage
   constexpr int kLoads = R * (NL + (WK ? 1 : 0));        // weight loads per wave and stage
-  constexpr int kWait = C * kLoads;
+  constexpr int kWait = D * kLoads;                      // and of the whole ring
   static_assert(kWait < 64, "the wait fits the counter");
-  constexpr int U = 2 * C > D ? 2 * C : D;               // stages per pass of the unrolled loop
-  __shared__ __attribute__((aligned(1024))) uint8_t xb0[kBuf];
-  __shared__ __attribute__((aligned(1024))) uint8_t xb1[kBuf];
+  __shared__ __attribute__((aligned(1024))) uint8_t xb[2 * kBuf];
   __shared__ int last_flag;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -220,13 +241,14 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   };
 
   // ---- activations.  A copy takes four rows x 256 bytes: lane l row l / 16,
-  // piece (l % 16) ^ (row % 8) of 16 bytes, so that the lanes reading one
-  // piece of eight rows hit different banks.  Rows past the group and bytes
+  // piece (l % 16) ^ (row % 16) of 16 bytes, so that the lanes reading one
+  // piece of 16 rows hit different banks.  Rows past the group and bytes
   // past the row take an offset beyond the resource and land as zeros. ----
   constexpr int kQ = 4 * T;                           // copies of a stage
-  constexpr int kPer = C * kQ / NW;                   // copies of a buffer per wave
+  constexpr int kPer = D * kQ / NW;                   // copies of a buffer per wave
   constexpr int kRowsPer = kQ >= NW ? kQ / NW : 1;    // different rows among them
-  static_assert(C * kQ % NW == 0 && (kQ % NW == 0 || NW % kQ == 0), "every wave copies the same share");
+  static_assert(NW % 4 == 0, "a wave's copies have the same rows modulo 16");
+  static_assert(D * kQ % NW == 0 && (kQ % NW == 0 || NW % kQ == 0), "every wave copies the same share");
   const int64_t xrow0 = a.rows ? 0 : row0;
   const int64_t xrows = a.rows ? a.M : cnt;
   const i32x4 xr = rsrc_words(a.X + xrow0 * a.ldx, (uint32_t)((xrows - 1) * a.ldx + a.xbytes));
@@ -237,7 +259,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
     return q < 0 || q >= a.M ? 0xFFFFFFFFu : (uint32_t)q;
   };
   const int q0 = kQ >= NW ? wave : wave % kQ;
-  const int cr = lane >> 4, piece = (lane & 15) ^ ((4 * (q0 & 1) + cr) & 7);
+  const int cr = lane >> 4, piece = (lane & 15) ^ (4 * (q0 & 3) + cr);
   uint32_t xo[kRowsPer];
 #pragma unroll
   for (int i = 0; i < kRowsPer; ++i) {
@@ -245,7 +267,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
     xo[i] = r == 0xFFFFFFFFu ? kOutOfRange : r * (uint32_t)a.ldx + 16u * piece;
   }
   // exponent bytes of mx4 activations: a copy takes 16 rows x 16 bytes
-  constexpr int kSPer = XK ? (C * T + NW - 1) / NW : 1;
+  constexpr int kSPer = XK ? (D * T + NW - 1) / NW : 1;
   uint32_t xso[kSPer];
   i32x4 xsr{};
   if constexpr (XK) {
@@ -256,23 +278,23 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
       xso[i] = r == 0xFFFFFFFFu ? kOutOfRange : r * (uint32_t)a.ldxs + 4u * (lane & 3);
     }
   }
-  // buffer m: stages C m .. C m + C - 1 of this split
-  auto copy_x = [&](int m, uint8_t* buf) __attribute__((always_inline)) {
+  // stages c .. c + D - 1 of this split into a buffer
+  auto copy_x = [&](int c, uint32_t buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int q = kQ >= NW ? wave + NW * (i % kRowsPer) : q0;
       const int st = kQ >= NW ? i / kRowsPer : wave / kQ + i * (NW / kQ);
-      const int at = lo + m * C + st;  // stage of K
+      const int at = lo + c + st;  // stage of K
       const int left = (int)a.xbytes - at * kStageBytes;
       const uint32_t v = 16 * piece >= left || at >= hi ? kOutOfRange : xo[i % kRowsPer];
-      copy16<false>(xr, lds_addr(buf) + st * kStage + q * 1024u, v, (uint32_t)(at < hi ? at * kStageBytes : 0));
+      copy16<false>(xr, buf + st * kStage + q * 1024u, v, (uint32_t)(at < hi ? at * kStageBytes : 0));
     }
     if constexpr (XK) {
 #pragma unroll
       for (int i = 0; i < kSPer; ++i) {
-        const int id = wave + NW * i, st = id / T, at = lo + m * C + st;
-        if (id < C * T)
-          copy4<false>(xsr, lds_addr(buf) + C * kStage + id * 256u, at >= hi ? kOutOfRange : xso[i],
+        const int id = wave + NW * i, st = id / T, at = lo + c + st;
+        if (id < D * T)
+          copy4<false>(xsr, buf + D * kStage + id * 256u, at >= hi ? kOutOfRange : xso[i],
                        (uint32_t)(at < hi ? at * 16 : 0));
       }
     }
@@ -282,7 +304,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   const int fr = lane & 15;
   auto frag_off = [&](int i) __attribute__((always_inline)) -> uint32_t {
     const int pc = WK && !XK ? 4 * g + i : 4 * i + g;
-    return (uint32_t)(fr * kStageBytes + 16 * (pc ^ (fr & 7)));
+    return (uint32_t)(fr * kStageBytes + 16 * (pc ^ fr));
   };
   uint32_t fo[4];
 #pragma unroll
@@ -294,36 +316,37 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  copy_x(0, xb0);
+  const uint32_t xlds = lds_addr(xb);
+  copy_x(0, xlds);
   static_for<0, D>([&](auto sl) __attribute__((always_inline)) {
-    constexpr int c = decltype(sl)::value;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      load_s(sl, r, c);
+      load_s(sl, r, decltype(sl)::value);
 #pragma unroll
-      for (int i = 0; i < NL; ++i) load_w(sl, r, i, c);
+      for (int i = 0; i < NL; ++i) load_w(sl, r, i, decltype(sl)::value);
     }
   });
-  // the copies are older than the D stages of weights
-  constexpr int kFirst = D * kLoads;
-  __builtin_amdgcn_s_waitcnt((int)((kFirst & 15) | ((kFirst >> 4) << 14) | (7 << 4) | (0 << 8)));
-  barrier_no_fence();
+  // waits until this wave's copies have landed: at most a ring of weight loads
+  // is younger than they are
+  auto ready = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt((int)((kWait & 15) | ((kWait >> 4) << 14) | (7 << 4) | (0 << 8)));
+    barrier_no_fence();
+  };
+  ready();
 
-  for (int c0 = 0; c0 < n; c0 += U) {
+  uint32_t cur = 0;  // the buffer to read
+  for (int c0 = 0; c0 < n; c0 += D) {
+    if (c0 + D < n) copy_x(c0 + D, xlds + (kBuf - cur));
     bool done = false;
-    static_for<0, U>([&](auto ic) __attribute__((always_inline)) {
-      constexpr int i = decltype(ic)::value;
-      constexpr int slot = i % D, buf = (i / C) & 1, at = i % C;
+    static_for<0, D>([&](auto sl) __attribute__((always_inline)) {
+      constexpr int i = decltype(sl)::value;
       const int c = c0 + i;
-      if (done || c >= n) {
+      if (i > 0 && (done || c >= n)) {
         done = true;
         return;
       }
-      if constexpr (at == 0) {
-        if (c + C < n) copy_x((c0 + i) / C + 1, buf ? xb0 : xb1);
-      }
-      const uint8_t* xs = (buf ? xb1 : xb0) + at * kStage;
-      const uint8_t* xe = (buf ? xb1 : xb0) + C * kStage + at * kScales;
+      const uint8_t* xs = xb + cur + i * kStage;
+      const uint8_t* xe = xb + cur + D * kStage + i * kScales;
       uint32_t sb[XK ? T : 1];
       if constexpr (XK) {
 #pragma unroll
@@ -332,47 +355,64 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
       float wsc[WK && !XK ? R : 1];
       if constexpr (WK && !XK) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) wsc[r] = exp_scale((sc[slot][r] >> (8 * ((lo + c) & 3))) & 255u);
+        for (int r = 0; r < R; ++r) wsc[r] = exp_scale((sc[i][r] >> (8 * ((lo + c) & 3))) & 255u);
       }
-      static_for<0, 4>([&](auto jc) __attribute__((always_inline)) {
-        constexpr int q = decltype(jc)::value;
-        bf16x8 A[R];
-        if constexpr (!XK) {
+      // The stage's 4 T activation operands, in steps of one operand and its R
+      // products; operands are read PF steps ahead of their products, and the
+      // widened weights of a quarter are made during the quarter before.
+      constexpr int PF = 4 * T > 8 ? 3 : 2;
+      u32x4 b[PF + 1];
+      auto read_b = [&](auto kc) __attribute__((always_inline)) {
+        constexpr int k = decltype(kc)::value;
+        if constexpr (k < 4 * T) b[k % (PF + 1)] = *(const u32x4*)(xs + (k % T) * (16 * kStageBytes) + fo[k / T]);
+      };
+      bf16x8 A[2][R];
+      auto widen = [&](auto qc, int r) __attribute__((always_inline)) {
+        constexpr int q = decltype(qc)::value;
+        if constexpr (!XK && q < 4) {
+          if constexpr (WK) A[q & 1][r] = mx4x8_to_bf16(w[i][r][0][q], wsc[r]);
+          else A[q & 1][r] = as_bf16x8(w[i][r][q]);
+        }
+      };
+      static_for<0, PF>(read_b);
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if constexpr (WK) A[r] = mx4x8_to_bf16(w[slot][r][0][q], wsc[r]);
-            else A[r] = as_bf16x8(w[slot][r][q]);
+      for (int r = 0; r < R; ++r) widen(std::integral_constant<int, 0>{}, r);
+      static_for<0, 4 * T>([&](auto kc) __attribute__((always_inline)) {
+        constexpr int k = decltype(kc)::value, q = k / T, t = k % T;
+        read_b(std::integral_constant<int, k + PF>{});
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if constexpr (XK) acc[r][t] = mfma_mx4<q>(w[i][r][q], b[k % (PF + 1)], acc[r][t], sc[i][r], sb[t]);
+          else acc[r][t] = mfma_bf16(A[q & 1][r], as_bf16x8(b[k % (PF + 1)]), acc[r][t]);
+        }
+        if constexpr (WK && !XK) {
+#pragma unroll
+          for (int r = t * R / T; r < (t + 1) * R / T; ++r) widen(std::integral_constant<int, q + 1>{}, r);
+        }
+        if constexpr (t == T - 1) {
+          // refill what this quarter was the last to read
+          if constexpr (!WK) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) widen(std::integral_constant<int, q + 1>{}, r);
+          }
+          if constexpr (NL == 4) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) load_w(sl, r, q, c + D);
+          }
+          if constexpr (q == 3) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if constexpr (NL == 1) load_w(sl, r, 0, c + D);
+              load_s(sl, r, c + D);
+            }
           }
         }
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-          const u32x4 b = *(const u32x4*)(xs + t * (16 * kStageBytes) + fo[q]);
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if constexpr (XK) acc[r][t] = mfma_mx4<q>(w[slot][r][q], b, acc[r][t], sc[slot][r], sb[t]);
-            else acc[r][t] = mfma_bf16(A[r], as_bf16x8(b), acc[r][t]);
-          }
-        }
-        // refill what this step was the last to read
-        if constexpr (NL == 4) {
-#pragma unroll
-          for (int r = 0; r < R; ++r) load_w(std::integral_constant<int, slot>{}, r, q, c + D);
-        }
-        if constexpr (q == 3) {
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if constexpr (NL == 1) load_w(std::integral_constant<int, slot>{}, r, 0, c + D);
-            load_s(std::integral_constant<int, slot>{}, r, c + D);
-          }
-        }
+        __builtin_amdgcn_sched_barrier(0);
       });
-      if constexpr (at == C - 1) {
-        // the other buffer's copies have landed (the weights loaded since stay
-        // in flight) and this buffer's reads are done
-        __builtin_amdgcn_s_waitcnt((int)((kWait & 15) | ((kWait >> 4) << 14) | (7 << 4) | (0 << 8)));
-        barrier_no_fence();
-      }
     });
+    // the other buffer has landed and this one's reads are done
+    ready();
+    cur = kBuf - cur;
   }
   SPENSE_WAIT_VM(0);
 
@@ -391,45 +431,52 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
         if (rt0 + r < d.NT && 16 * t + fr < cnt) store_partial(wsr, poff(s, rt0 + r, row0 + 16 * t + fr), acc[r][t]);
     if (!arrive_last(a.counters + (int64_t)j * p.rgroups + rg, S, &last_flag)) return;
   }
+  if (rt0 >= d.NT) return;
+  // every wave has left the activations' buffers
+  static_assert(NW * 16 * (64 * R + 16) <= 2 * kBuf, "the waves' parts of LDS");
+  uint8_t* part_lds = xb + wave * (16 * (64 * R + 16));
+  const bool wide = a.yvec;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (rt0 + r >= d.NT) break;
+  for (int t = 0; t < T; ++t) {
+    if (16 * t >= cnt) break;
+    const int64_t m = row0 + 16 * t + fr;
+    f32x4 v[R];
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      if (16 * t + fr >= cnt) continue;
-      const int64_t m = row0 + 16 * t + fr;
-      f32x4 v = acc[r][t];
+    for (int r = 0; r < R; ++r) {
+      v[r] = acc[r][t];
       if (S > 1) {
         // in split order, eight at a time (one memory round trip per eight)
-        v = f32x4{0.f, 0.f, 0.f, 0.f};
+        v[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const bool in = rt0 + r < d.NT && 16 * t + fr < cnt;
         for (int s0 = 0; s0 < S; s0 += 8) {
           f32x4 part[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) part[q] = load_partial(wsr, s0 + q < S ? poff(s0 + q, rt0 + r, m) : kOutOfRange);
+          for (int q = 0; q < 8; ++q)
+            part[q] = load_partial(wsr, in && s0 + q < S ? poff(s0 + q, rt0 + r, m) : kOutOfRange);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            if (s0 + q < S) v += part[q];
+            if (s0 + q < S) v[r] += part[q];
         }
       }
-      put_tile(d, a, m, (rt0 + r) * 16 + nb, v);
     }
+    put_rows<R>(d, a, v, part_lds, row0 + 16 * t, cnt - 16 * t, rt0 * (d.glu ? 8 : 16), wide);
   }
 }
 
-template <bool WK, bool XK, int NW, int R, int T, int C, int D, int WPS>
+template <bool WK, bool XK, int NW, int R, int T, int D, int WPS>
 hipError_t launch_k(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPlan& p, hipStream_t s) {
   if (p.rgroups != (d.NT + NW * R - 1) / (NW * R)) return hipErrorInvalidValue;
   const int64_t grid = (int64_t)p.rgroups * p.mgroups * p.splits;
   if (grid < 1 || grid * NW * 64 > 0x7FFFFFFF) return hipErrorInvalidValue;  // threads count in 32 bits
-  experts_kernel<WK, XK, NW, R, T, C, D, WPS><<<(unsigned)grid, NW * 64, 0, s>>>(d, a, p);
+  experts_kernel<WK, XK, NW, R, T, D, WPS><<<(unsigned)grid, NW * 64, 0, s>>>(d, a, p);
   return hipGetLastError();
 }
 
 template <bool WK, bool XK>
 hipError_t launch_t(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPlan& p, hipStream_t s) {
   switch (p.config) {
-#define SPENSE_EXPERT_CASE(i, nw, r, t, c, dd, wps) \
-  case i: return launch_k<WK, XK, nw, r, t, c, dd, wps>(d, a, p, s);
+#define SPENSE_EXPERT_CASE(i, nw, r, t, dd, wps) \
+  case i: return launch_k<WK, XK, nw, r, t, dd, wps>(d, a, p, s);
     SPENSE_EXPERT_CONFIGS(SPENSE_EXPERT_CASE)
 #undef SPENSE_EXPERT_CASE
     default: return hipErrorInvalidValue;
@@ -458,7 +505,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* X, int64_
 
 int experts_config_count() {
   int n = 0;
-#define SPENSE_EXPERT_COUNT(i, nw, r, t, c, dd, wps) ++n;
+#define SPENSE_EXPERT_COUNT(i, nw, r, t, dd, wps) ++n;
   SPENSE_EXPERT_CONFIGS(SPENSE_EXPERT_COUNT)
 #undef SPENSE_EXPERT_COUNT
   return n;
@@ -466,7 +513,7 @@ int experts_config_count() {
 
 ExpertsShape experts_shape(int config) {
   switch (config) {
-#define SPENSE_EXPERT_SHAPE(i, nw, r, t, c, dd, wps) \
+#define SPENSE_EXPERT_SHAPE(i, nw, r, t, dd, wps) \
   case i: return ExpertsShape{nw, r, t};
     SPENSE_EXPERT_CONFIGS(SPENSE_EXPERT_SHAPE)
 #undef SPENSE_EXPERT_SHAPE

@@ -49,7 +49,7 @@ ExpertsPlan make_plan(const ExpertsDesc& d, bool grouped, int64_t R, bool xmx) {
     if (f_config >= experts_config_count()) f_config = -1;
   }
   // the smallest m-tile count that takes an average expert's rows in one group
-  p.config = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 3 : 4;
+  p.config = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
   if (f_config >= 0) p.config = f_config;
   const ExpertsShape c = experts_shape(p.config);
   const int64_t per = c.waves * c.r, take = 16 * c.t;
@@ -186,7 +186,7 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
   a.Y = Y;
   a.ldy = ldy;
   a.ydtype = ydtype;
-  a.yvec = ((uintptr_t)Y & 15) == 0 && ldy % 4 == 0;
+  a.yvec = ((uintptr_t)Y & 15) == 0 && ldy * (ydtype == SPENSE_F32 ? 4 : 2) % 16 == 0;
   // The product kernel reads rows of 16-byte pieces through offsets of 31
   // bits: mx4 activations are quantised into that form, bf16 ones are read in
   // place if they have it and laid out first if not.  Rows picked from beyond
