@@ -31,9 +31,9 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 // Configurations: X(index, waves, row tiles per wave R, m-tiles T, stages D in
 // the ring and in an LDS buffer, waves per SIMD the registers allow)
 #define SPENSE_EXPERT_CONFIGS(X) \
-  X(0, 8, 1, 1, 4, 2)            \
-  X(1, 8, 1, 2, 4, 2)            \
-  X(2, 4, 2, 4, 2, 2)            \
+  X(0, 8, 1, 1, 8, 2)            \
+  X(1, 4, 1, 2, 4, 2)            \
+  X(2, 8, 1, 4, 2, 2)            \
   X(3, 4, 2, 8, 1, 2)            \
   X(4, 4, 4, 8, 1, 2)
 
@@ -83,6 +83,33 @@ __device__ __forceinline__ void find_group(const ExpertsDesc& d, const ExpertsAr
     }
     before += __builtin_amdgcn_readlane(incl, 63);
   }
+}
+
+// Split, row group and m-tile group of this workgroup; false past the last.
+// Workgroups are dealt to the 8 XCDs round robin; the workgroups of an XCD take
+// the tiles in runs of p.run, so that those running together there form a
+// block of p.rblock row groups x some m-groups and share both operands in the
+// XCD's L2 (experts' gate/up, 16 x 3200 x 5120 bf16, 8192 rows: 2.3 GB of L2
+// misses without the runs).
+__device__ __forceinline__ bool tile_of(const ExpertsPlan& p, int& s, int& rg, int& j) {
+  const uint32_t b = blockIdx.x, xcd = b % 8u, seq = b / 8u;
+  const uint32_t run = (uint32_t)p.run, lap = seq / run;
+  uint32_t id = (lap * 8u + xcd) * run + (seq - lap * run);
+  const uint32_t per = (uint32_t)p.rgroups * (uint32_t)p.mgroups;
+  s = 0;
+  if (p.splits > 1) {
+    s = (int)(id / per);
+    id -= (uint32_t)s * per;
+  }
+  if (s >= p.splits || id >= per) return false;
+  // blocks of rblock row groups (fewer in the last), one m-group after the other
+  const uint32_t span = (uint32_t)p.rblock * (uint32_t)p.mgroups;
+  const uint32_t blk = id / span, r0 = blk * (uint32_t)p.rblock, rem = id - blk * span;
+  const uint32_t left = (uint32_t)p.rgroups - r0, nb = left < (uint32_t)p.rblock ? left : (uint32_t)p.rblock;
+  const uint32_t m = rem / nb;
+  j = (int)m;
+  rg = (int)(r0 + rem - m * nb);
+  return true;
 }
 
 // exponent byte -> the power of two (255 -> NaN)
@@ -170,6 +197,61 @@ __device__ __forceinline__ void put_rows(const ExpertsDesc& d, const ExpertsArgs
   }
 }
 
+// LDS of a wave in put_rows
+template <int R>
+constexpr uint32_t kPartLds = 16 * (64 * R + 16);
+
+// The end of a wave's R row tiles (rt0 ..) x T m-tiles (rows row0 .. row0 + cnt
+// - 1 of Y): with split K the sums go to the workspace and the workgroup that
+// arrives last adds them in split order.  Lane l holds the sums of packed rows
+// 4 (l / 16) + 0..3 of a row tile at row l % 16 of an m-tile.  cnt may be zero
+// or negative.
+template <int R, int T>
+__device__ __forceinline__ void finish(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPlan& p,
+                                       const f32x4 (&acc)[R][T], uint8_t* lds, int s, int rg, int j, int64_t rt0,
+                                       int64_t row0, int cnt, int* last_flag) {
+  const int lane = threadIdx.x & 63, fr = lane & 15, nb = 4 * (lane >> 4);
+  const int S = p.splits;
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws, S > 1 ? (uint32_t)((int64_t)S * d.NT * a.R * 64) : 0u);
+  auto poff = [&](int64_t split, int64_t rt, int64_t m) {
+    return (uint32_t)((((split * d.NT + rt) * a.R + m) * 16 + nb) * 4);
+  };
+  if (S > 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        if (rt0 + r < d.NT && 16 * t + fr < cnt) store_partial(wsr, poff(s, rt0 + r, row0 + 16 * t + fr), acc[r][t]);
+    if (!arrive_last(a.counters + (int64_t)j * p.rgroups + rg, S, last_flag)) return;
+  }
+  if (rt0 >= d.NT) return;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    if (16 * t >= cnt) break;
+    const int64_t m = row0 + 16 * t + fr;
+    f32x4 v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      v[r] = acc[r][t];
+      if (S > 1) {
+        // in split order, eight at a time (one memory round trip per eight)
+        v[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const bool in = rt0 + r < d.NT && 16 * t + fr < cnt;
+        for (int s0 = 0; s0 < S; s0 += 8) {
+          f32x4 part[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            part[q] = load_partial(wsr, in && s0 + q < S ? poff(s0 + q, rt0 + r, m) : kOutOfRange);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (s0 + q < S) v[r] += part[q];
+        }
+      }
+    }
+    put_rows<R>(d, a, v, lds, row0 + 16 * t, cnt - 16 * t, rt0 * (d.glu ? 8 : 16), a.yvec);
+  }
+}
+
 // WK: bf16 (false) or mx4 (true) weights; XK: the same of the activations
 template <bool WK, bool XK, int NW, int R, int T, int D, int WPS>
 __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, ExpertsArgs a, ExpertsPlan p) {
@@ -182,6 +264,11 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   constexpr int kLoads = R * (NL + (WK ? 1 : 0));        // weight loads per wave and stage
   constexpr int kWait = D * kLoads;                      // and of the whole ring
   static_assert(kWait < 64, "the wait fits the counter");
+  // With one stage in the ring its copies are spread over the products of the
+  // first three quarters (in one go they hold up the LDS reads beside them),
+  // and a stage's weights that come in one load are loaded a stage ahead.
+  constexpr bool kSpread = D == 1, kAhead = kSpread && NL == 1;
+  constexpr int kYoung = kAhead ? 0 : kSpread ? 2 * R + (WK ? R : 0) : kWait;  // weight loads after the last copy
   __shared__ __attribute__((aligned(1024))) uint8_t xb[2 * kBuf];
   __shared__ int last_flag;
   const int lane = threadIdx.x & 63;
@@ -191,15 +278,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   // ---- which tile ----
   const int S = p.splits;
   int s, rg, j;
-  {
-    LinearPlan q{};
-    q.splits = S;
-    q.rgroups = p.rgroups;
-    q.mgroups = p.mgroups;
-    q.rblock = p.rblock;
-    q.xcd_remap = gridDim.x % 8 == 0;
-    tile_coords(blockIdx.x, gridDim.x, q, s, rg, j);
-  }
+  if (!tile_of(p, s, rg, j)) return;
   int e, cnt;
   int64_t row0;
   find_group(d, a, kRows, j, e, row0, cnt);
@@ -218,8 +297,9 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   const __amdgpu_buffer_rsrc_t wr =
       make_rsrc(d.wpack + ((int64_t)e * d.NT + (nrt ? rt0 : 0)) * d.tile_bytes, (uint32_t)(nrt * d.tile_bytes));
   const uint32_t tb = (uint32_t)d.tile_bytes, so = (uint32_t)d.scale_off;
-  u32x4 w[D][R][NL];
-  uint32_t sc[D][WK ? R : 1];
+  constexpr int kSlots = kAhead ? 2 : D;
+  u32x4 w[kSlots][R][NL];
+  uint32_t sc[kSlots][WK ? R : 1];
   auto load_w = [&](auto slot, int r, int i, int c) __attribute__((always_inline)) {
     const int st = lo + c;
     uint32_t off = (uint32_t)r * tb;
@@ -278,26 +358,27 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
       xso[i] = r == 0xFFFFFFFFu ? kOutOfRange : r * (uint32_t)a.ldxs + 4u * (lane & 3);
     }
   }
-  // stages c .. c + D - 1 of this split into a buffer
-  auto copy_x = [&](int c, uint32_t buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+  // copy number i (a compile-time index) of this wave's share of stages c ..
+  // c + D - 1 of the split: first the rows, then the exponent bytes
+  constexpr int kCopies = kPer + (XK ? kSPer : 0);
+  auto copy_one = [&](int c, uint32_t buf, auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    if constexpr (i < kPer) {
       const int q = kQ >= NW ? wave + NW * (i % kRowsPer) : q0;
       const int st = kQ >= NW ? i / kRowsPer : wave / kQ + i * (NW / kQ);
       const int at = lo + c + st;  // stage of K
       const int left = (int)a.xbytes - at * kStageBytes;
       const uint32_t v = 16 * piece >= left || at >= hi ? kOutOfRange : xo[i % kRowsPer];
       copy16<false>(xr, buf + st * kStage + q * 1024u, v, (uint32_t)(at < hi ? at * kStageBytes : 0));
+    } else {
+      const int id = wave + NW * (i - kPer), st = id / T, at = lo + c + st;
+      if (D * T % NW == 0 || id < D * T)
+        copy4<false>(xsr, buf + D * kStage + id * 256u, at >= hi ? kOutOfRange : xso[i - kPer],
+                     (uint32_t)(at < hi ? at * 16 : 0));
     }
-    if constexpr (XK) {
-#pragma unroll
-      for (int i = 0; i < kSPer; ++i) {
-        const int id = wave + NW * i, st = id / T, at = lo + c + st;
-        if (id < D * T)
-          copy4<false>(xsr, buf + D * kStage + id * 256u, at >= hi ? kOutOfRange : xso[i],
-                       (uint32_t)(at < hi ? at * 16 : 0));
-      }
-    }
+  };
+  auto copy_x = [&](int c, uint32_t buf) __attribute__((always_inline)) {
+    static_for<0, kCopies>([&](auto ic) __attribute__((always_inline)) { copy_one(c, buf, ic); });
   };
 
   // this lane's piece of row lane % 16 for step i
@@ -326,17 +407,28 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
       for (int i = 0; i < NL; ++i) load_w(sl, r, i, decltype(sl)::value);
     }
   });
-  // waits until this wave's copies have landed: at most a ring of weight loads
-  // is younger than they are
-  auto ready = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt((int)((kWait & 15) | ((kWait >> 4) << 14) | (7 << 4) | (0 << 8)));
+  // Waits until this wave's copies have landed (at most `young` weight loads
+  // are younger than they are) and its LDS reads are done, then for the others.
+  auto ready = [&](auto young) __attribute__((always_inline)) {
+    constexpr int v = decltype(young)::value;
+    __builtin_amdgcn_s_waitcnt((int)((v & 15) | ((v >> 4) << 14) | (7 << 4) | (0 << 8)));
     barrier_no_fence();
   };
-  ready();
+  ready(std::integral_constant<int, kWait>{});
 
   uint32_t cur = 0;  // the buffer to read
   for (int c0 = 0; c0 < n; c0 += D) {
-    if (c0 + D < n) copy_x(c0 + D, xlds + (kBuf - cur));
+    const uint32_t other = xlds + (kBuf - cur);
+    if constexpr (!kSpread) {
+      if (c0 + D < n) copy_x(c0 + D, other);
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        load_w(std::integral_constant<int, 1>{}, r, 0, c0 + 1);
+        load_s(std::integral_constant<int, 1>{}, r, c0 + 1);
+      }
+    }
     bool done = false;
     static_for<0, D>([&](auto sl) __attribute__((always_inline)) {
       constexpr int i = decltype(sl)::value;
@@ -385,16 +477,17 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
           if constexpr (XK) acc[r][t] = mfma_mx4<q>(w[i][r][q], b[k % (PF + 1)], acc[r][t], sc[i][r], sb[t]);
           else acc[r][t] = mfma_bf16(A[q & 1][r], as_bf16x8(b[k % (PF + 1)]), acc[r][t]);
         }
-        if constexpr (WK && !XK) {
+        if constexpr (!XK) {
 #pragma unroll
           for (int r = t * R / T; r < (t + 1) * R / T; ++r) widen(std::integral_constant<int, q + 1>{}, r);
         }
-        if constexpr (t == T - 1) {
+        if constexpr (kSpread && k < 3 * T) {
+          // past the last stage they write zeros: no branch in the loop
+          static_for<k * kCopies / (3 * T), (k + 1) * kCopies / (3 * T)>(
+              [&](auto ic) __attribute__((always_inline)) { copy_one(c0 + D, other, ic); });
+        }
+        if constexpr (t == T - 1 && !kAhead) {
           // refill what this quarter was the last to read
-          if constexpr (!WK) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) widen(std::integral_constant<int, q + 1>{}, r);
-          }
           if constexpr (NL == 4) {
 #pragma unroll
             for (int r = 0; r < R; ++r) load_w(sl, r, q, c + D);
@@ -411,64 +504,35 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
       });
     });
     // the other buffer has landed and this one's reads are done
-    ready();
+    ready(std::integral_constant<int, kYoung>{});
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        w[0][r][0] = w[1][r][0];
+        sc[0][r] = sc[1][r];
+      }
+    }
     cur = kBuf - cur;
   }
   SPENSE_WAIT_VM(0);
 
-  // ---- epilogue: lane l holds sums of packed rows 4 (l / 16) + 0..3 of a row
-  // tile at activation row l % 16 of an m-tile ----
-  const int nb = 4 * g;
-  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws, S > 1 ? (uint32_t)((int64_t)S * d.NT * a.R * 64) : 0u);
-  auto poff = [&](int64_t split, int64_t rt, int64_t m) {
-    return (uint32_t)((((split * d.NT + rt) * a.R + m) * 16 + nb) * 4);
-  };
-  if (S > 1) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-        if (rt0 + r < d.NT && 16 * t + fr < cnt) store_partial(wsr, poff(s, rt0 + r, row0 + 16 * t + fr), acc[r][t]);
-    if (!arrive_last(a.counters + (int64_t)j * p.rgroups + rg, S, &last_flag)) return;
-  }
-  if (rt0 >= d.NT) return;
-  // every wave has left the activations' buffers
-  static_assert(NW * 16 * (64 * R + 16) <= 2 * kBuf, "the waves' parts of LDS");
-  uint8_t* part_lds = xb + wave * (16 * (64 * R + 16));
-  const bool wide = a.yvec;
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-    if (16 * t >= cnt) break;
-    const int64_t m = row0 + 16 * t + fr;
-    f32x4 v[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      v[r] = acc[r][t];
-      if (S > 1) {
-        // in split order, eight at a time (one memory round trip per eight)
-        v[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const bool in = rt0 + r < d.NT && 16 * t + fr < cnt;
-        for (int s0 = 0; s0 < S; s0 += 8) {
-          f32x4 part[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            part[q] = load_partial(wsr, in && s0 + q < S ? poff(s0 + q, rt0 + r, m) : kOutOfRange);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (s0 + q < S) v[r] += part[q];
-        }
-      }
-    }
-    put_rows<R>(d, a, v, part_lds, row0 + 16 * t, cnt - 16 * t, rt0 * (d.glu ? 8 : 16), wide);
-  }
+  static_assert(NW * kPartLds<R> <= 2 * kBuf, "the waves' parts of LDS");
+  finish<R, T>(d, a, p, acc, xb + wave * kPartLds<R>, s, rg, j, rt0, row0, cnt, &last_flag);
+}
+
+// grid of a plan, 0 if it does not fit
+unsigned grid_of(const ExpertsDesc& d, const ExpertsPlan& p, int per, int threads) {
+  if (p.rgroups != (d.NT + per - 1) / per || p.run < 1 || p.rblock < 1) return 0;
+  const int64_t tiles = (int64_t)p.rgroups * p.mgroups * p.splits;
+  const int64_t grid = (tiles + 8 * p.run - 1) / (8 * p.run) * (8 * p.run);
+  return grid < 1 || grid * threads > 0x7FFFFFFF ? 0u : (unsigned)grid;  // threads count in 32 bits
 }
 
 template <bool WK, bool XK, int NW, int R, int T, int D, int WPS>
 hipError_t launch_k(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPlan& p, hipStream_t s) {
-  if (p.rgroups != (d.NT + NW * R - 1) / (NW * R)) return hipErrorInvalidValue;
-  const int64_t grid = (int64_t)p.rgroups * p.mgroups * p.splits;
-  if (grid < 1 || grid * NW * 64 > 0x7FFFFFFF) return hipErrorInvalidValue;  // threads count in 32 bits
-  experts_kernel<WK, XK, NW, R, T, D, WPS><<<(unsigned)grid, NW * 64, 0, s>>>(d, a, p);
+  const unsigned grid = grid_of(d, p, NW * R, NW * 64);
+  if (!grid) return hipErrorInvalidValue;
+  experts_kernel<WK, XK, NW, R, T, D, WPS><<<grid, NW * 64, 0, s>>>(d, a, p);
   return hipGetLastError();
 }
 
@@ -514,10 +578,10 @@ int experts_config_count() {
 ExpertsShape experts_shape(int config) {
   switch (config) {
 #define SPENSE_EXPERT_SHAPE(i, nw, r, t, dd, wps) \
-  case i: return ExpertsShape{nw, r, t};
+  case i: return ExpertsShape{nw, r, t, dd};
     SPENSE_EXPERT_CONFIGS(SPENSE_EXPERT_SHAPE)
 #undef SPENSE_EXPERT_SHAPE
-    default: return ExpertsShape{0, 0, 0};
+    default: return ExpertsShape{0, 0, 0, 0};
   }
 }
 

@@ -71,12 +71,13 @@ struct ExpertsPlan {
   int rgroups;  // groups of row tiles, one per workgroup
   int mgroups;  // groups of activation rows (upper bound over the experts)
   int rblock;   // row groups taken together before the next m-group (launch order)
+  int run;      // consecutive tiles that one XCD takes
 };
 
 // A configuration of the product kernel: waves per workgroup, row tiles per
-// wave, m-tiles (16 activation rows).
+// wave, m-tiles (16 activation rows), stages in flight.
 struct ExpertsShape {
-  int waves, r, t;
+  int waves, r, t, stages;
 };
 int experts_config_count();
 ExpertsShape experts_shape(int config);

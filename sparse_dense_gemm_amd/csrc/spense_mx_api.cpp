@@ -2,6 +2,7 @@
 // workspaces.  Arguments have been checked by the entry points in
 // spense_api.cpp.
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <new>
@@ -36,37 +37,91 @@ int status_of(hipError_t e) {
   return e == hipErrorOutOfMemory ? SPENSE_ENOMEM : rc;
 }
 
+// Estimated cycles of a launch of `groups` m-groups.  Per stage (256 bytes of
+// every activation row) a workgroup multiplies 4 waves r t operand pairs at 16
+// cycles on each of four SIMDs and moves its weights and activations through
+// the CU's vector cache at 64 bytes a cycle; the two hardly overlap (55296 x
+// 5120 at 2048 rows: products alone 210 us, with either operand's loads 260,
+// with both 310).  A stage takes at least the memory latency over the stages
+// in flight, and the launch the time its weights take from memory.  Two
+// workgroups run together on a CU.  With split K every sum is written and read
+// once more, and a workgroup reads its tile's S sums by itself.
+double plan_cycles(const ExpertsDesc& d, int config, int64_t S, double groups, int64_t hit, int64_t R, bool xmx) {
+  const ExpertsShape c = experts_shape(config);
+  const bool mx = d.wdtype == SPENSE_MX4;
+  const double wkb = (mx ? (xmx ? 4.25 : 1.25) : 4.0) * c.waves * c.r, xkb = 4.0 * c.t;
+  // small m-tiles pay a barrier and their epilogue per fewer products
+  const double work = (16.0 * c.waves * c.r * c.t + 16.0 * (wkb + xkb)) * (c.t < 4 ? 1.3 : c.t == 4 ? 1.45 : 1.0) + 60.0;
+  // with one stage in the ring, weights of four loads wait behind its copies
+  const double latency = c.stages > 1 ? 3000.0 / c.stages : mx && !xmx ? 2000.0 : 5000.0;
+  const int64_t rg = (d.NT + c.waves * c.r - 1) / (c.waves * c.r);
+  const int64_t stages = ((xmx ? (d.NU + 3) / 4 : d.NU) + S - 1) / S;
+  const int64_t load = (int64_t)std::ceil((double)rg * groups * (double)S / kCUs);  // workgroups of the fullest CU
+  double t = (double)(load / 2) * std::max(2.0 * work, latency) + (load % 2 ? std::max(1.3 * work, latency) : 0.0);
+  t = std::max(t * (double)stages, (double)(hit * d.NT * d.tile_bytes) / 2600.0);
+  t += 3000.0 * (double)((load + 1) / 2);
+  if (S > 1) {
+    const double tile = 1024.0 * c.waves * c.r * c.t;  // bytes of a workgroup's sums
+    t += 4000.0 + (double)(S + 1) * tile / 40.0 + (double)(S * d.NT * 16 * R) * 8.0 / 1500.0;
+  }
+  return t;
+}
+
 // Launch plan of R grouped rows (a function of ceil(R / 16) only, so that the
-// workspaces of every smaller call can be sized by stepping over it).
+// workspaces of every smaller call can be sized by stepping over it): of the
+// kernel's configurations and the split counts that fill one or two workgroups
+// per CU, the one with the least estimated time.
 ExpertsPlan make_plan(const ExpertsDesc& d, bool grouped, int64_t R, bool xmx) {
-  const int64_t R16 = (R + 15) / 16 * 16;
-  const int64_t hit = grouped ? std::min(d.E, R16) : 1;  // experts that may have rows
-  const int64_t rows = (R16 + hit - 1) / hit;            // rows of one, on average
-  ExpertsPlan p{};
   int f_config = -1, f_splits = 0, f_rblock = 0;  // forced by SPENSE_EXPERTS=config[,splits[,rblock]] (tests, tuning)
   if (const char* v = getenv("SPENSE_EXPERTS")) {
     sscanf(v, "%d,%d,%d", &f_config, &f_splits, &f_rblock);
     if (f_config >= experts_config_count()) f_config = -1;
   }
-  // the smallest m-tile count that takes an average expert's rows in one group
-  p.config = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
-  if (f_config >= 0) p.config = f_config;
-  const ExpertsShape c = experts_shape(p.config);
-  const int64_t per = c.waves * c.r, take = 16 * c.t;
-  p.rgroups = (int)((d.NT + per - 1) / per);
-  // sum over experts of ceil(n / take) for any split of R rows over `hit` experts
-  p.mgroups = (int)(grouped ? (R16 - hit) / take + hit : (R16 + take - 1) / take);
-  // split K where the tiles alone leave CUs without a workgroup
+  const int64_t R16 = (R + 15) / 16 * 16;
+  const int64_t hit = grouped ? std::min(d.E, R16) : 1;  // experts that may have rows
+  const int64_t rows = (R16 + hit - 1) / hit;            // rows of one, on average
   const int64_t stages = xmx ? (d.NU + 3) / 4 : d.NU;
-  const int64_t tiles = (int64_t)p.rgroups * p.mgroups;
-  const int64_t want = c.t <= 4 ? 2 * kCUs : kCUs;
-  int64_t S = tiles >= want ? 1 : (want + tiles / 2) / tiles;
-  S = std::min<int64_t>({S, std::max<int64_t>(1, stages / (xmx ? 2 : 4)), 64});
-  if (f_splits > 0) S = std::min<int64_t>(f_splits, std::min<int64_t>(stages, 64));
-  while (S > 1 && S * d.NT * R16 * 64 > kMaxPartials) --S;
-  p.splits = (int)S;
-  p.rblock = c.t >= 8 && p.mgroups > 1 ? 8 : 1;
+  ExpertsPlan p{};
+  double best = 0.0;
+  for (int i = 0; i < experts_config_count(); ++i) {
+    if (f_config >= 0 && i != f_config) continue;
+    const ExpertsShape c = experts_shape(i);
+    const int64_t per = c.waves * c.r, take = 16 * c.t;
+    const int64_t rg = (d.NT + per - 1) / per;
+    // sum over experts of ceil(n / take) for any split of R rows over `hit` experts
+    const int64_t mg = grouped ? (R16 - hit) / take + hit : (R16 + take - 1) / take;
+    // of them with rows: groups of no particular size leave half of their last m-group empty
+    const double busy =
+        grouped && hit > 1 ? (double)hit * std::max(1.0, (double)rows / (double)take + 0.5) : (double)mg;
+    const int64_t most = std::min<int64_t>(std::max<int64_t>(1, stages / (xmx ? 2 : 4)), 64);
+    int64_t tried = 0;
+    for (int k = 0; k <= 2; ++k) {
+      int64_t S = k == 0 ? 1 : std::min<int64_t>(most, (int64_t)(k * kCUs / ((double)rg * busy)));
+      if (f_splits > 0) S = std::min<int64_t>(f_splits, std::min<int64_t>(stages, 64));
+      while (S > 1 && S * d.NT * R16 * 64 > kMaxPartials) --S;
+      if (S <= tried) continue;
+      tried = S;
+      const double t = plan_cycles(d, i, S, busy, hit, R16, xmx);
+      if (best == 0.0 || t < best) {
+        best = t;
+        p.config = i;
+        p.splits = (int)S;
+        p.rgroups = (int)rg;
+        p.mgroups = (int)mg;
+      }
+    }
+  }
+  const ExpertsShape c = experts_shape(p.config);
+  // Launch order: large groups in blocks of four row groups, m-group by m-group
+  // (the two workgroups of a CU, 32 apart, then share their row group's
+  // weights: experts' gate/up of 8192 rows 307 us, blocks of 13 row groups
+  // 339); small ones, whose weights are most of what is read, m-group by
+  // m-group of a single row group.  An XCD takes runs of consecutive tiles,
+  // every XCD as many.
+  p.rblock = c.t >= 8 ? (int)std::min(p.rgroups, 4) : 1;
   if (f_rblock > 0) p.rblock = f_rblock;
+  const int64_t all = (int64_t)p.rgroups * p.mgroups * p.splits, laps = (all + 511) / 512;
+  p.run = (int)((all + 8 * laps - 1) / (8 * laps));
   return p;
 }
 

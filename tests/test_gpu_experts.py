@@ -150,3 +150,44 @@ def test_graph_replays_follow_the_offsets():
         h(X, off, eager, rows=rows)
         torch.cuda.synchronize()
         assert torch.equal(Y, eager) and not Y.isnan().any()
+
+
+@pytest.mark.parametrize("w,a", KINDS, ids=lambda k: k)
+@pytest.mark.parametrize("config", range(5))
+def test_every_configuration_and_split(config, w, a, monkeypatch):
+    """Each shape of the product kernel, with one and several splits of K, and other launch orders."""
+    h, W = experts_case(3, 300, 1900, sdg.DT_MX4 if w == "mx4" else sdg.DT_BF16, False, 11)
+    rng = np.random.default_rng(11)
+    X = dev(rng.standard_normal((60, 1900)).astype(np.float32)).bfloat16()
+    rows = rng.integers(0, 60, 290)
+    ad = sdg.DT_MX4 if a == "mx4" else sdg.DT_BF16
+    for plan in ("1", "2,1", "3,7", "4,3", "64"):
+        monkeypatch.setenv("SPENSE_EXPERTS", f"{config},{plan}")
+        check(h, W, X, [0, 17, 17, 287], rows, 290, False, ad, label=(config, plan))
+    monkeypatch.setenv("SPENSE_EXPERTS", f"{config},2")
+    outs = [torch.empty((290, 300), dtype=torch.float32, device="cuda") for _ in range(2)]
+    for y in outs:
+        h(X, dev(np.array([0, 17, 17, 290], dtype=np.int32)), y, rows=dev(rows.astype(np.int32)), adtype=ad)
+    assert torch.equal(*outs)
+
+
+def test_rows_past_31_bits_of_offset():
+    """Activations of more than 2 GB: picked rows are gathered first, grouped ones read in place."""
+    M, K, N = 300000, 4096, 32
+    h, W = experts_case(2, N, K, sdg.DT_MX4, False, 12)
+    X = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(12)
+    pick = np.array([0, M - 1, 262143, 262144, 262145, 7])
+    X[torch.from_numpy(pick).cuda()] = dev(rng.standard_normal((6, K)).astype(np.float32)).bfloat16()
+    xs = X[torch.from_numpy(pick).cuda()].float().cpu().numpy().astype(np.float64)
+    for ad in (sdg.DT_BF16, sdg.DT_MX4):
+        xr = xs if ad == sdg.DT_BF16 else oracle.mx4_values_ref(*oracle.mx4_quantize_ref(xs), K)
+        ref, B = oracle.experts_linear_ref(xr, W, [0, 2, 6])
+        Y = torch.empty((6, N), dtype=torch.float32, device="cuda")
+        h(X, dev(np.array([0, 2, 6], dtype=np.int32)), Y, rows=dev(pick.astype(np.int32)), adtype=ad)
+        assert (np.abs(Y.cpu().numpy() - ref) <= (K / 32 + 160) * 2.0 ** -23 * B).all()
+        # grouped already, the last rows beyond the offset
+        Yb = torch.empty((M, N), dtype=torch.float32, device="cuda")
+        h(X, dev(np.array([0, 5, M], dtype=np.int32)), Yb, adtype=ad)
+        last, B = oracle.product_ref(xr[1:2], W[1])
+        assert (np.abs(Yb[M - 1:].cpu().numpy() - last) <= (K / 32 + 160) * 2.0 ** -23 * B).all()
