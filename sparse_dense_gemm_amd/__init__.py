@@ -133,24 +133,34 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        return _torch().cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def dtype_of(t) -> int:
-    import torch
+_torch_module = None
+_dtypes = {}
 
-    if t.dtype == torch.float32:
-        return DT_F32
-    if t.dtype == torch.bfloat16:
-        return DT_BF16
-    if t.dtype in (torch.float8_e4m3fn, torch.uint8):
-        return DT_FP8
-    raise TypeError(f"unsupported dtype {t.dtype}")
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+        _dtypes.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float8_e4m3fn: DT_FP8,
+                        torch.uint8: DT_FP8})
+    return _torch_module
+
+
+def dtype_of(t) -> int:
+    if not _dtypes:
+        _torch()
+    d = _dtypes.get(t.dtype)
+    if d is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return d
 
 
 def spense_pack(W, wdtype: Optional[int] = None, *, scales=None, dense_cols=None, dense_fraction: float = 0.0,
@@ -348,12 +358,11 @@ def spense_dequantize_mx4(codes, scales, Y, *, ydtype: Optional[int] = None, str
 
 
 def _mx4_shape(codes, scales, rows: int, K: int) -> None:
-    if (codes.shape[0] < rows or scales.shape[0] < rows or codes.shape[1] < (K + 1) // 2
-            or scales.shape[1] < (K + 31) // 32):
-        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold {rows} x {K} mx4")
-    for t in (codes, scales):
-        if t.element_size() != 1 or t.stride(1) != 1:
-            raise ValueError("codes and scales are bytes, contiguous along a row")
+    c, s = codes.shape, scales.shape
+    if c[0] < rows or s[0] < rows or c[1] < (K + 1) // 2 or s[1] < (K + 31) // 32:
+        raise ValueError(f"codes {tuple(c)} and scales {tuple(s)} do not hold {rows} x {K} mx4")
+    if codes.element_size() != 1 or scales.element_size() != 1 or codes.stride(1) != 1 or scales.stride(1) != 1:
+        raise ValueError("codes and scales are bytes, contiguous along a row")
 
 
 def spense_pack_mx4(codes, scales, *, N: Optional[int] = None, K: Optional[int] = None, stream=None) -> int:

@@ -51,24 +51,55 @@ __device__ __forceinline__ int block_scan(int v, int* tmp) {
   return v + before;
 }
 
-// The choices of TB tokens.  G lanes share a token, V logits each.  With one
-// block of tokens (fused) it also writes offsets, rows and final places;
-// otherwise the block's counts and each choice's place within the block.
-template <int G, int V>
-__global__ __launch_bounds__(256) void choose_kernel(RouteArgs a, int TB, int fused) {
+// Largest value / smallest index over the G lanes that share a token.  Within
+// rows of 16 lanes the operands move with the instruction (row rotations).
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  auto take = [&](uint32_t o) { v = o > v ? o : v; };
+  take(row_ror<0x128>(v));
+  take(row_ror<0x124>(v));
+  take(row_ror<0x122>(v));
+  take(row_ror<0x121>(v));
+  if constexpr (G == 64) {
+    take((uint32_t)__shfl_xor((int)v, 16));
+    take((uint32_t)__shfl_xor((int)v, 32));
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return ~group_max<G>(~v);
+}
+
+constexpr int kHeld = 4096;  // choices of a block that are kept in LDS
+
+// The choices of TB tokens.  G lanes share a token, V logits each; choice j is
+// kept by lane j % G until the weights' sum is known.  With one block of tokens
+// (fused) it also writes offsets, rows and final places; otherwise the block's
+// counts and each choice's place within the block.
+template <int G, int V, int NT>
+__global__ __launch_bounds__(NT) void choose_kernel(RouteArgs a, int TB, int fused) {
   extern __shared__ uint32_t bits[];  // [E][TB / 32], then (fused) [E] first rows
   __shared__ int tmp[16], last;
+  __shared__ int16_t held[kHeld];
   const int words = TB / 32;
   const int E = (int)a.E;
-  for (int i = threadIdx.x; i < E * words; i += 256) bits[i] = 0u;
+  const bool hold = TB * a.k <= kHeld;
+  for (int i = threadIdx.x; i < E * words; i += NT) bits[i] = 0u;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * TB;
+  const int64_t left = a.T - t0;
+  const int have = left < TB ? (int)left : TB;  // tokens of this block
   const int sub = threadIdx.x % G;
-  constexpr int kTokens = 256 / G;  // tokens at a time
-  for (int tb = 0; tb < TB; tb += kTokens) {
+  constexpr int kTokens = NT / G;  // tokens at a time
+  for (int tb = 0; tb < have; tb += kTokens) {
     const int tl = tb + threadIdx.x / G;
     const int64_t t = t0 + tl;
-    const bool in = t < a.T;
+    const bool in = tl < have;
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -77,63 +108,65 @@ __global__ __launch_bounds__(256) void choose_kernel(RouteArgs a, int TB, int fu
     }
     // softmax over every expert that may be taken, if the weights are not
     // renormalised over the chosen ones
-    float total = 0.f, top = 0.f;
+    float sum = 0.f, top = 0.f;
     if (!a.renormalize) {
       uint32_t m = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) m = key[v] > m ? key[v] : m;
-#pragma unroll
-      for (int o = 1; o < G; o <<= 1) {
-        const uint32_t x = (uint32_t)__shfl_xor((int)m, o, G);
-        m = x > m ? x : m;
-      }
-      top = key_logit(m);
+      top = key_logit(group_max<G>(m));
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (key[v]) total += weight_of(key_logit(key[v]), top);
+        if (key[v]) sum += weight_of(key_logit(key[v]), top);
 #pragma unroll
-      for (int o = 1; o < G; o <<= 1) total += __shfl_xor(total, o, G);
+      for (int o = 1; o < G; o <<= 1) sum += __shfl_xor(sum, o, G);
     }
-    float chosen = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t m = 0;
-      int e = 0;
+    for (int j0 = 0; j0 < a.k; j0 += G) {  // once for k <= G
+      int my_e = -1;
+      float my_w = 0.f;
+      const int j1 = a.k - j0 < G ? a.k - j0 : G;
+      for (int j = 0; j < j1; ++j) {
+        uint32_t m = 0;
 #pragma unroll
-      for (int v = V - 1; v >= 0; --v)
-        if (key[v] >= m) {  // equal keys: the lower expert
-          m = key[v];
-          e = sub + G * v;
-        }
+        for (int v = 0; v < V; ++v) m = key[v] > m ? key[v] : m;
+        m = group_max<G>(m);
+        uint32_t e = 0xFFFFFFFFu;
 #pragma unroll
-      for (int o = 1; o < G; o <<= 1) {
-        const uint32_t m2 = (uint32_t)__shfl_xor((int)m, o, G);
-        const int e2 = __shfl_xor(e, o, G);
-        if (m2 > m || (m2 == m && e2 < e)) {
-          m = m2;
-          e = e2;
+        for (int v = V - 1; v >= 0; --v)
+          if (key[v] == m) e = sub + G * v;  // equal keys: the lower expert
+        e = group_min<G>(e);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (e == (uint32_t)(sub + G * v)) key[v] = 0u;
+        if (a.renormalize && j0 + j == 0) top = key_logit(m);
+        if (m == 0u) break;
+        if (sub == j) {
+          my_e = (int)e;
+          my_w = weight_of(key_logit(m), top);
         }
       }
+      if (a.renormalize) {
+        float s = my_w;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e == sub + G * v) key[v] = 0u;
-      if (a.renormalize && j == 0) top = key_logit(m);
-      const float w = m ? weight_of(key_logit(m), top) : 0.f;
-      chosen += w;
-      if (in && sub == 0) {
-        a.ids[t * a.k + j] = m ? e : -1;
-        a.weights[t * a.k + j] = w;
-        if (m) atomicOr(&bits[e * words + (tl >> 5)], 1u << (tl & 31));
+        for (int o = 1; o < G; o <<= 1) s += __shfl_xor(s, o, G);
+        sum += s;
+      }
+      if (in && sub < j1) {
+        const int64_t at = t * a.k + j0 + sub;
+        a.ids[at] = my_e;
+        a.weights[at] = a.renormalize && a.k > G ? my_w : my_e < 0 ? 0.f : my_w / sum;
+        if (hold) held[tl * a.k + j0 + sub] = (int16_t)my_e;
+        if (my_e >= 0) atomicOr(&bits[my_e * words + (tl >> 5)], 1u << (tl & 31));
       }
     }
-    const float sum = a.renormalize ? chosen : total;
-    if (in && sub == 0 && sum > 0.f)
-      for (int j = 0; j < a.k; ++j) a.weights[t * a.k + j] /= sum;
+    // more choices than lanes: the sum is known only now (a lane reads what it wrote)
+    if (a.renormalize && a.k > G && in && sum > 0.f)
+      for (int j = sub; j < a.k; j += G) a.weights[t * a.k + j] /= sum;
   }
   __syncthreads();
   // counts, and (fused) the experts' first rows
   int* first = (int*)(bits + E * words);
   int carry = 0;
-  for (int e0 = 0; e0 < E; e0 += 256) {
+  for (int e0 = 0; e0 < E; e0 += NT) {
     const int e = e0 + threadIdx.x;
     int n = 0;
     if (e < E)
@@ -147,18 +180,17 @@ __global__ __launch_bounds__(256) void choose_kernel(RouteArgs a, int TB, int fu
         a.offsets[e] = incl - n;
         if (e == E - 1) a.offsets[E] = incl;
       }
-      if (threadIdx.x == 255) last = incl;
+      if (threadIdx.x == NT - 1) last = incl;
       __syncthreads();
       carry = last;
       __syncthreads();
     }
   }
-  const int64_t left = a.T - t0;
-  const int pairs = (int)((left < TB ? left : TB) * a.k);
-  for (int i = threadIdx.x; i < pairs; i += 256) {
+  const int pairs = have * a.k;
+  for (int i = threadIdx.x; i < pairs; i += NT) {
     const int tl = i / a.k;
     const int64_t at = t0 * a.k + i;
-    const int e = a.ids[at];
+    const int e = hold ? held[i] : a.ids[at];
     int place = -1;
     if (e >= 0) {
       place = __popc(bits[e * words + (tl >> 5)] & ((1u << (tl & 31)) - 1u));
@@ -171,53 +203,65 @@ __global__ __launch_bounds__(256) void choose_kernel(RouteArgs a, int TB, int fu
     a.pos[at] = place;
   }
   if (fused)
-    for (int64_t r = carry + threadIdx.x; r < a.T * a.k; r += 256) a.rows[r] = -1;
+    for (int64_t r = carry + threadIdx.x; r < a.T * a.k; r += NT) a.rows[r] = -1;
 }
 
 // Places of one block's choices: the counts of all blocks give the experts'
 // first rows, those of the blocks before this one its own start among them.
-__global__ __launch_bounds__(256) void place_kernel(RouteArgs a, int TB, int blocks) {
+// The threads split the blocks among them, P threads to an expert: what bounds
+// it is the latency of a thread's reads in a row (8191 tokens, 128 experts: 62
+// us of router with one thread to an expert and no reads ahead).
+constexpr int kPlace = 1024;  // threads of place_kernel
+__global__ __launch_bounds__(kPlace) void place_kernel(RouteArgs a, int TB, int blocks, int P) {
   extern __shared__ int base[];  // [E]
-  __shared__ int tmp[16], last;
+  __shared__ int tmp[16], last, all_s[kPlace], before_s[kPlace];
   const int E = (int)a.E;
   const int b = blockIdx.x;
+  const int per = kPlace / P, part = threadIdx.x / per;  // experts at a time; share of the blocks
   int carry = 0;
-  for (int e0 = 0; e0 < E; e0 += 256) {
-    const int e = e0 + threadIdx.x;
+  for (int e0 = 0; e0 < E; e0 += per) {
+    const int e = e0 + threadIdx.x % per;
     int all = 0, before = 0;
-    if (e < E)
-      for (int i = 0; i < blocks; ++i) {
+    if (e < E) {
+#pragma unroll 8
+      for (int i = part; i < blocks; i += P) {
         const int n = a.work[(int64_t)i * E + e];
         all += n;
         before += i < b ? n : 0;
       }
-    const int incl = block_scan(all, tmp) + carry;
-    if (e < E) {
+    }
+    all_s[threadIdx.x] = all;
+    before_s[threadIdx.x] = before;
+    __syncthreads();
+    all = before = 0;
+    if (part == 0)
+      for (int q = 0; q < P; ++q) {
+        all += all_s[threadIdx.x + q * per];
+        before += before_s[threadIdx.x + q * per];
+      }
+    const int incl = block_scan(all, tmp) + carry;  // zeros beyond the first part
+    if (part == 0 && e < E) {
       base[e] = incl - all + before;
       if (b == 0) {
         a.offsets[e] = incl - all;
         if (e == E - 1) a.offsets[E] = incl;
       }
     }
-    if (threadIdx.x == 255) last = incl;
+    if (threadIdx.x == kPlace - 1) last = incl;
     __syncthreads();
     carry = last;
     __syncthreads();
   }
   const int64_t t0 = (int64_t)b * TB, left = a.T - t0;
   const int pairs = (int)((left < TB ? left : TB) * a.k);
-  for (int i = threadIdx.x; i < pairs; i += 256) {
+  for (int i = threadIdx.x; i < pairs; i += kPlace) {
     const int64_t at = t0 * a.k + i;
     const int e = a.ids[at];
+    if (at >= carry) a.rows[at] = -1;  // rows past the last choice
     if (e < 0) continue;
     const int place = a.pos[at] + base[e];
     a.pos[at] = place;
     a.rows[place] = (int)(t0 + i / a.k);
-  }
-  // rows past the last choice
-  for (int i = threadIdx.x; i < pairs; i += 256) {
-    const int64_t r = t0 * a.k + i;
-    if (r >= carry) a.rows[r] = -1;
   }
 }
 
@@ -282,19 +326,23 @@ __global__ void no_rows_kernel(int32_t* offsets, int64_t E) {
   if (i <= E) offsets[i] = 0;
 }
 
-// Tokens of a block: 64, more for so many tokens that reading every block's
-// counts (blocks^2 E) would cost more than the tokens do, as far as the bits
-// take 48 KB of LDS.
+// Tokens of a block.  Up to 256 tokens run as one block in one launch; more
+// take the smallest blocks that leave at most 256 (each block reads every
+// block's counts), as far as the bits take 48 KB of LDS.
 int tokens_per_block(int64_t T, int64_t E) {
-  int TB = T <= (int64_t(1) << 14) ? 64 : T <= (int64_t(1) << 17) ? 256 : 1024;
-  while (TB > 64 && E * (TB / 8) > 48 * 1024) TB /= 2;
+  if (T <= 256 && E * 32 <= 48 * 1024) return 256;
+  int TB = 32;
+  while (TB < 1024 && (T + TB - 1) / TB > 256 && E * (TB / 4) <= 48 * 1024) TB *= 2;
   return TB;
 }
 
 template <int G, int V>
 hipError_t choose(const RouteArgs& a, int TB, int blocks, hipStream_t s) {
   const size_t lds = (size_t)a.E * (TB / 32) * 4 + (blocks == 1 ? (size_t)a.E * 4 : 0);
-  choose_kernel<G, V><<<blocks, 256, lds, s>>>(a, TB, blocks == 1);
+  // one block: 1024 threads where the tokens keep them busy
+  if (blocks == 1 && a.T * G > 256) choose_kernel<G, V, 1024><<<1, 1024, lds, s>>>(a, TB, 1);
+  else if (blocks == 1) choose_kernel<G, V, 256><<<1, 256, lds, s>>>(a, TB, 1);
+  else choose_kernel<G, V, 512><<<blocks, 512, lds, s>>>(a, TB, 0);
   return hipGetLastError();
 }
 
@@ -322,7 +370,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   else if (a.E <= 512) e = choose<64, 8>(a, TB, blocks, s);
   else e = choose<64, 16>(a, TB, blocks, s);
   if (e != hipSuccess || blocks == 1) return e;
-  place_kernel<<<blocks, 256, (size_t)a.E * 4, s>>>(a, TB, blocks);
+  int P = 1;  // threads to an expert: all of them at work
+  while (P < 64 && a.E * 2 * P <= kPlace) P *= 2;
+  place_kernel<<<blocks, kPlace, (size_t)a.E * 4, s>>>(a, TB, blocks, P);
   return hipGetLastError();
 }
 

@@ -78,7 +78,7 @@ def test_null_handles():
     assert lib.spense_experts_linear(None, P, BF16, 1, 64, None, P, 1, P, F32, 16, None) == EINVAL
 
 
-def route(logits=P, t=F32, T=200, E=8, ldl=8, k=2, ids=P, weights=P, offsets=P, rows=P, pos=P, work=P):
+def route(logits=P, t=F32, T=20000, E=8, ldl=8, k=2, ids=P, weights=P, offsets=P, rows=P, pos=P, work=P):
     return sdg._lib().spense_route(logits, t, T, E, ldl, k, 1, ids, weights, offsets, rows, pos, work, None)
 
 
