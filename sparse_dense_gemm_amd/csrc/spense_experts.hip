@@ -148,7 +148,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// the reciprocal instruction and the fast exponential are good to an ulp or two of 32 bits
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
 
 // Sixteen activation rows of a wave's R row tiles into Y.  A lane holds four
 // packed rows of each tile (v[r]), four output columns or two gated ones; its
@@ -550,9 +553,10 @@ hipError_t launch_t(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPla
 // Rows of bf16 into rows of ldo bytes, columns from K on zero; eight columns a thread.
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
                                                        const int32_t* rows, int64_t R, uint8_t* out, int64_t ldo) {
-  const int64_t per = ldo / 16, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= R * per) return;
-  const int64_t r = id / per, k = (id - r * per) * 8;
+  const uint32_t per = (uint32_t)(ldo / 16), id = blockIdx.x * 256u + threadIdx.x;  // at most 2^30 threads
+  const uint32_t row = id / per;
+  if (row >= R) return;
+  const int64_t r = row, k = (int64_t)(id - row * per) * 8;
   const int64_t src = rows ? rows[r] : r;
   uint16_t v[8];
 #pragma unroll

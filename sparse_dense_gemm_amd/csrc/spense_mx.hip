@@ -82,8 +82,9 @@ __global__ __launch_bounds__(256) void quantize_kernel(const XT* X, int64_t M, i
                                                        const int32_t* rows, int64_t R, uint8_t* codes, int64_t ldc,
                                                        uint8_t* scales, int64_t lds, int64_t blocks, bool vec,
                                                        bool cvec) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t b = id >> 2, row = b / blocks, col = b - row * blocks;
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;  // a launch has at most 2^30 threads
+  const uint32_t b = id >> 2, brow = b / (uint32_t)blocks;
+  const int64_t row = brow, col = b - brow * (uint32_t)blocks;
   const int q = (int)(id & 3);
   const bool in = row < R;
   const int64_t src = !in ? -1 : rows ? rows[row] : row;
@@ -126,8 +127,9 @@ template <typename YT>
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, int64_t ldc, const uint8_t* scales,
                                                          int64_t lds, int64_t M, int64_t K, YT* Y, int64_t ldy,
                                                          bool vec, bool cvec) {
-  const int64_t per = (K + 7) / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = id / per, k = (id - row * per) * 8;
+  const uint32_t per = (uint32_t)((K + 7) / 8), id = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t r = id / per;
+  const int64_t row = r, k = (int64_t)(id - r * per) * 8;
   if (row >= M) return;
   const uint8_t* in = codes + row * ldc + k / 2;
   uint32_t c = 0;

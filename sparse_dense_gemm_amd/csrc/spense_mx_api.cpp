@@ -72,9 +72,10 @@ double plan_cycles(const ExpertsDesc& d, int config, int64_t S, double groups, i
 // kernel's configurations and the split counts that fill one or two workgroups
 // per CU, the one with the least estimated time.
 ExpertsPlan make_plan(const ExpertsDesc& d, bool grouped, int64_t R, bool xmx) {
-  int f_config = -1, f_splits = 0, f_rblock = 0;  // forced by SPENSE_EXPERTS=config[,splits[,rblock]] (tests, tuning)
+  // forced by SPENSE_EXPERTS=config[,splits[,rblock[,run]]] (tests, tuning)
+  int f_config = -1, f_splits = 0, f_rblock = 0, f_run = 0;
   if (const char* v = getenv("SPENSE_EXPERTS")) {
-    sscanf(v, "%d,%d,%d", &f_config, &f_splits, &f_rblock);
+    sscanf(v, "%d,%d,%d,%d", &f_config, &f_splits, &f_rblock, &f_run);
     if (f_config >= experts_config_count()) f_config = -1;
   }
   const int64_t R16 = (R + 15) / 16 * 16;
@@ -117,11 +118,16 @@ ExpertsPlan make_plan(const ExpertsDesc& d, bool grouped, int64_t R, bool xmx) {
   // weights: experts' gate/up of 8192 rows 307 us, blocks of 13 row groups
   // 339); small ones, whose weights are most of what is read, m-group by
   // m-group of a single row group.  An XCD takes runs of consecutive tiles,
-  // every XCD as many.
+  // every XCD as many: 64 at most, what runs on it together; grouped rows
+  // shorter ones, since the m-groups that no expert fills are the last of each
+  // block and would leave some XCDs with less (gate/up of 8192 rows: runs of 43
+  // 311 us, of 16 276 us).
   p.rblock = c.t >= 8 ? (int)std::min(p.rgroups, 4) : 1;
   if (f_rblock > 0) p.rblock = f_rblock;
   const int64_t all = (int64_t)p.rgroups * p.mgroups * p.splits, laps = (all + 511) / 512;
   p.run = (int)((all + 8 * laps - 1) / (8 * laps));
+  if (grouped) p.run = std::min(p.run, c.t >= 8 ? 16 : 8);
+  if (f_run > 0) p.run = f_run;
   return p;
 }
 

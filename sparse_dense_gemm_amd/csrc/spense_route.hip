@@ -270,8 +270,9 @@ template <typename OT>
 __global__ __launch_bounds__(256) void combine_kernel(const OT* O, int64_t R, int64_t ldo, const int32_t* pos,
                                                       const float* weights, int64_t T, int64_t k, int64_t N, void* Y,
                                                       int32_t ydtype, int64_t ldy, bool vec) {
-  const int64_t per = (N + 3) / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t t = id / per, n = (id - t * per) * 4;
+  const uint32_t per = (uint32_t)((N + 3) / 4), id = blockIdx.x * 256u + threadIdx.x;  // at most 2^30 threads
+  const uint32_t row = id / per;
+  const int64_t t = row, n = (int64_t)(id - row * per) * 4;
   if (t >= T) return;
   f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int64_t j = 0; j < k; ++j) {
