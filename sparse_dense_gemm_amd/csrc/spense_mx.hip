@@ -185,11 +185,11 @@ __device__ __forceinline__ int64_t packed_row(const ExpertsDesc& d, int64_t r) {
 // each, of row tiles t0 .. t0 + tiles - 1 counted over the experts.
 template <bool MX>
 __global__ __launch_bounds__(256) void pack_experts_kernel(ExpertsDesc d, int64_t t0, int64_t tiles, const uint8_t* W,
-                                                           int64_t ldw) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                           int64_t ldw, bool vec) {
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;  // a launch has at most 2^30 threads
   const int lane = (int)(id & 63);
-  const int64_t per = MX ? d.NU : 4 * d.NU;  // kilobytes of a row tile
-  const int64_t kb = id >> 6, i = kb / per, u = kb - i * per;
+  const uint32_t per = (uint32_t)(MX ? d.NU : 4 * d.NU);  // kilobytes of a row tile
+  const uint32_t kb = id >> 6, i = kb / per, u = kb - i * per;
   if (i >= tiles) return;
   const int64_t tile = t0 + i;
   const int64_t e = tile / d.NT, rt = tile - e * d.NT;
@@ -203,31 +203,39 @@ __global__ __launch_bounds__(256) void pack_experts_kernel(ExpertsDesc d, int64_
   o.v = u32x4{0, 0, 0, 0};
   if (src >= 0) {
     if constexpr (MX) {
-      const int64_t k = u * kUnitK + 32 * g;
+      const int64_t k = (int64_t)u * kUnitK + 32 * g;
       const uint8_t* w = W + (e * d.N + src) * ldw + k / 2;
+      if (vec && k + 32 <= d.K) {
+        o.v = *(const u32x4*)w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (k + 2 * i + 1 < d.K) o.b[i] = w[i];
-        else if (k + 2 * i < d.K) o.b[i] = w[i] & 15;
+        for (int q = 0; q < 16; ++q) {
+          if (k + 2 * q + 1 < d.K) o.b[q] = w[q];
+          else if (k + 2 * q < d.K) o.b[q] = w[q] & 15;
+        }
       }
     } else {
-      const int64_t k = u * 32 + 8 * g;
+      const int64_t k = (int64_t)u * 32 + 8 * g;
       const uint16_t* w = (const uint16_t*)W + (e * d.N + src) * ldw + k;
+      if (vec && k + 8 <= d.K) {
+        o.v = *(const u32x4*)w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k + i < d.K) o.h[i] = w[i];
+        for (int q = 0; q < 8; ++q)
+          if (k + q < d.K) o.h[q] = w[q];
+      }
     }
   }
-  *(u32x4*)(d.wpack + tile * d.tile_bytes + u * 1024 + lane * 16) = o.v;
+  *(u32x4*)(d.wpack + tile * d.tile_bytes + (int64_t)u * 1024 + lane * 16) = o.v;
 }
 
 // One thread per lane and four units: their exponent bytes.
 __global__ __launch_bounds__(256) void pack_exponents_kernel(ExpertsDesc d, int64_t t0, int64_t tiles,
                                                              const uint8_t* scales, int64_t lds) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;
   const int lane = (int)(id & 63);
-  const int64_t per = (d.NU + 3) / 4;
-  const int64_t q = id >> 6, i = q / per, i4 = q - i * per;
+  const uint32_t per = (uint32_t)((d.NU + 3) / 4);
+  const uint32_t q = id >> 6, i = q / per, i4 = q - i * per;
   if (i >= tiles) return;
   const int64_t tile = t0 + i;
   const int64_t e = tile / d.NT, rt = tile - e * d.NT;
@@ -235,11 +243,11 @@ __global__ __launch_bounds__(256) void pack_exponents_kernel(ExpertsDesc d, int6
   uint32_t o = 0;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int64_t b = (4 * i4 + u) * 4 + (lane >> 4);  // block of 32 columns
+    const int64_t b = (4 * (int64_t)i4 + u) * 4 + (lane >> 4);  // block of 32 columns
     const uint32_t v = src >= 0 && b * kMxBlock < d.K ? scales[(e * d.N + src) * lds + b] : 127u;
     o |= v << (8 * u);
   }
-  *(uint32_t*)(d.wpack + tile * d.tile_bytes + d.scale_off + i4 * 256 + lane * 4) = o;
+  *(uint32_t*)(d.wpack + tile * d.tile_bytes + d.scale_off + (int64_t)i4 * 256 + lane * 4) = o;
 }
 
 bool aligned(const void* p, int64_t ld_bytes, int n) { return ((uintptr_t)p | (uintptr_t)ld_bytes) % n == 0; }
@@ -311,12 +319,13 @@ hipError_t launch_pack_experts(const ExpertsDesc& d, const void* W, int64_t ldw,
                                hipStream_t s) {
   const bool mx = d.wdtype == DT_MX4;
   const int64_t per = d.NU * (mx ? 64 : 256), per4 = (d.NU + 3) / 4 * 64;
+  const bool vec = aligned(W, mx ? ldw : 2 * ldw, 16);
   return by_rows(d.E * d.NT, per, [&](int64_t t0, int64_t n) {
     if (mx) {
-      pack_experts_kernel<true><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw);
+      pack_experts_kernel<true><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw, vec);
       pack_exponents_kernel<<<groups(n * per4), 256, 0, s>>>(d, t0, n, scales, lds);
     } else {
-      pack_experts_kernel<false><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw);
+      pack_experts_kernel<false><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw, vec);
     }
   });
 }
