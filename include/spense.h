@@ -415,7 +415,7 @@ int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, in
  * (or silu(gate) * up).  Only these rows of Y are written; an expert may have
  * none of them, or all.
  *
- *   X        device pointer, [M, ldx] bf16, ldx >= K.
+ *   X        device pointer, [M, ldx] bf16, ldx >= K, 1 <= M <= 2^24 (M = 0 only with R = 0).
  *   adtype   SPENSE_BF16: the activations as they are; SPENSE_MX4: quantised in the
  *            call (mx4 weights only).
  *   rows     device pointer, [R] int32 rows of X, or NULL (then M >= R); a row
@@ -425,7 +425,9 @@ int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, in
  *   Y        device pointer, [R, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16), ldy >= N (I).
  * The sizes of the groups stay on the device.  Deterministic; workspaces,
  * asynchrony and graph capture as for spense_linear (R and M at most those of
- * the eager call, with the same adtype and with rows given or not).
+ * the eager call, with the same adtype, rows given or not alike and X aligned
+ * alike: rows of X that do not start at 16 bytes, or a K that is no multiple of
+ * 8, are laid out in the workspace first).
  */
 int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_t M, int64_t ldx, const int32_t* rows,
                           const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, void* stream);
@@ -445,7 +447,8 @@ int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_
  *            choice) grouped by expert, in token order; row r of expert e,
  *            offsets[e] <= r < offsets[e + 1], is token rows[r], and choice j of
  *            token t is row pos[t, j] (-1: missing).  rows is -1 past offsets[E].
- *   work     spense_route_workspace(T, E, k) bytes, 4-byte aligned, may be NULL if 0.
+ *   work     spense_route_workspace(T, E, k) bytes (enough for fewer tokens too), 4-byte aligned,
+ *            may be NULL if 0.
  * All device pointers.  Deterministic, asynchronous on `stream`, graph-capturable,
  * no state kept: calls with workspaces of their own may overlap.
  */

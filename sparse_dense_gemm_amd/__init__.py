@@ -133,22 +133,27 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        torch = _torch()
+        if _raw_stream is not None:  # the handle itself, without a Stream object around it (0.1 instead of 2.7 us)
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 _torch_module = None
+_raw_stream = None
 _dtypes = {}
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _raw_stream
     if _torch_module is None:
         import torch
 
         _torch_module = torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _dtypes.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float8_e4m3fn: DT_FP8,
                         torch.uint8: DT_FP8})
     return _torch_module

@@ -1347,14 +1347,15 @@ int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_
                           const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, void* stream) {
   if (!h || h->split != 4 || !X || !offsets || !Y) return SPENSE_EINVAL;
   const ExpertsDesc& d = experts_desc(h->experts);
-  if (M < 0 || M > (int64_t(1) << 24) || R < 0 || R > (int64_t(1) << 24) || (!rows && M < R)) return SPENSE_EINVAL;
+  if (M < (R ? 1 : 0) || M > (int64_t(1) << 24) || R < 0 || R > (int64_t(1) << 24)) return SPENSE_EINVAL;
+  if (!rows && M < R) return SPENSE_EINVAL;
   if (ldx < d.K || ldy < (d.glu ? d.N / 2 : d.N)) return SPENSE_EINVAL;
   if (adtype != SPENSE_BF16 && adtype != SPENSE_MX4)
     return valid_dtype(adtype) ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
   if (ydtype != SPENSE_F32 && ydtype != SPENSE_BF16)
     return ydtype == SPENSE_FP8_E4M3 || ydtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
   if (ldx >= kMaxLd || (adtype == SPENSE_MX4 && d.wdtype != SPENSE_MX4)) return SPENSE_EUNSUPPORTED;
-  if (R == 0 || M == 0) return SPENSE_OK;
+  if (R == 0) return SPENSE_OK;
   return experts_run(h->experts, X, adtype, M, ldx, rows, offsets, R, Y, ydtype, ldy, (hipStream_t)stream);
 }
 

@@ -23,6 +23,9 @@ struct ExpertsLayer {
   size_t ws_bytes = 0;
   int32_t* counters = nullptr;
   size_t n_counters = 0;
+  // rows that ws and counters have been sized for, whatever split count a
+  // smaller call's plan takes: [mx4 activations][grouped]
+  int64_t sized[2][2] = {{0, 0}, {0, 0}};
 };
 
 namespace {
@@ -273,12 +276,15 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
       need.xws = n_rows * a.ldx;
     }
   }
+  int64_t& sized = h->sized[xmx][offsets != nullptr];
+  if (R > sized) {  // every smaller call too: none of them may allocate later (graph capture)
+    for (int64_t r = (sized / 16 + 1) * 16; r < R; r += 16) need.grow(plan_need(d, make_plan(d, offsets != nullptr, r, xmx), r));
+  }
   if (!fits(h, need)) {
-    for (int64_t r = 16; r < R; r += 16)  // every smaller call too, whichever of its rows it brings
-      need.grow(plan_need(d, make_plan(d, offsets != nullptr, r, xmx), r));
     const int rc = grow(h, need, s);
     if (rc != SPENSE_OK) return rc;
   }
+  sized = std::max(sized, R);
   hipError_t e = hipSuccess;
   a.M = M;
   if (prepare) {

@@ -11,6 +11,8 @@
 // result does not depend on it.  One launch for a single block of tokens, else
 // two: the first leaves each block's counts in the workspace, the second adds
 // up the counts of the blocks before its own.
+#include <algorithm>
+
 #include "spense_device.h"
 #include "spense_mx.h"
 
@@ -349,10 +351,12 @@ hipError_t choose(const RouteArgs& a, int TB, int blocks, hipStream_t s) {
 
 }  // namespace
 
+// Counts of every block, for T tokens or any smaller number (whose blocks may
+// be smaller and more).
 int64_t route_work_bytes(int64_t T, int64_t E) {
-  const int TB = tokens_per_block(T, E);
-  const int64_t blocks = (T + TB - 1) / TB;
-  return blocks <= 1 ? 0 : blocks * E * 4;
+  if (T <= tokens_per_block(T, E)) return 0;
+  const int64_t blocks = (T + tokens_per_block(T, E) - 1) / tokens_per_block(T, E);
+  return std::max(blocks, std::min<int64_t>((T + 31) / 32, 256)) * E * 4;
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {

@@ -97,6 +97,10 @@ def test_route_workspace():
     lib = sdg._lib()
     assert lib.spense_route_workspace(1, 8, 2) == 0 and lib.spense_route_workspace(64, 8, 2) == 0
     assert lib.spense_route_workspace(100000, 128, 8) > 0
+    # enough for every smaller number of tokens
+    for E in (3, 128, 1000):
+        sizes = [lib.spense_route_workspace(T, E, 2) for T in list(range(0, 3000)) + list(range(3000, 300000, 997))]
+        assert sizes == sorted(sizes)
     for T, E, k in ((-1, 8, 2), (1, 0, 1), (1, 8, 9), (1, 2000, 1)):
         assert lib.spense_route_workspace(T, E, k) == EINVAL
         with pytest.raises(sdg.SpenseError):

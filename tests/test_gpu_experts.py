@@ -191,3 +191,62 @@ def test_rows_past_31_bits_of_offset():
         h(X, dev(np.array([0, 5, M], dtype=np.int32)), Yb, adtype=ad)
         last, B = oracle.product_ref(xr[1:2], W[1])
         assert (np.abs(Yb[M - 1:].cpu().numpy() - last) <= (K / 32 + 160) * 2.0 ** -23 * B).all()
+
+
+def test_one_eager_call_sizes_every_smaller_one():
+    """Captures at smaller sizes than one eager call allocate nothing, whatever split count they take."""
+    h, W = experts_case(4, 96, 4096, sdg.DT_MX4, False, 13)
+    X = dev(np.random.default_rng(13).standard_normal((900, 4096)).astype(np.float32)).bfloat16()
+    for ad in (sdg.DT_BF16, sdg.DT_MX4):
+        Y = torch.empty((900, 96), dtype=torch.float32, device="cuda")
+        off = dev(offsets_of([900, 0, 0, 0]))
+        h(X[:20], off, Y[:20], adtype=ad)
+        h(X, off, Y, adtype=ad)
+        torch.cuda.synchronize()
+        for R in (1, 17, 100, 333, 500, 777):
+            out = torch.empty((R, 96), dtype=torch.float32, device="cuda")
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                h(X[:R], off, out, adtype=ad)
+            for _ in range(2):
+                out.fill_(float("nan"))
+                graph.replay()
+                torch.cuda.synchronize()
+                h(X[:R], off, Y[:R], adtype=ad)
+                torch.cuda.synchronize()
+                assert torch.equal(out, Y[:R])
+
+
+def test_refusals_on_a_handle():
+    """Arguments that only a handle's sizes and types can refuse; nothing is written."""
+    h, _ = experts_case(2, 32, 64, sdg.DT_BF16, True, 14)
+    X = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    off = dev(np.array([0, 2, 4], dtype=np.int32))
+    Y = torch.full((4, 16), 7.0, device="cuda")
+    lib, ptr = sdg._lib(), [t.data_ptr() for t in (X, off, Y)]
+
+    def call(adtype=sdg.DT_BF16, M=4, ldx=64, R=4, yt=sdg.DT_F32, ldy=16, rows=None, handle=h.handle):
+        return lib.spense_experts_linear(handle, ptr[0], adtype, M, ldx, rows, ptr[1], R, ptr[2], yt, ldy, None)
+
+    bad, unsupported = sdg.SPENSE_EINVAL, sdg.SPENSE_EUNSUPPORTED
+    for kw, want in ((dict(M=0), bad), (dict(M=-1, R=0), bad), (dict(M=3), bad), (dict(M=0, rows=ptr[1]), bad),
+                     (dict(R=-1), bad), (dict(ldx=63), bad), (dict(ldy=15), bad), (dict(adtype=9), bad),
+                     (dict(yt=9), bad), (dict(adtype=sdg.DT_F32), unsupported), (dict(adtype=sdg.DT_MX4), unsupported),
+                     (dict(yt=sdg.DT_FP8), unsupported), (dict(R=0, M=0), sdg.SPENSE_OK)):
+        assert call(**kw) == want, kw
+    # the other entry points do not take an experts' handle, nor this one theirs
+    assert lib.spense_linear(h.handle, ptr[0], sdg.DT_BF16, 4, 64, ptr[2], sdg.DT_F32, 32, None) == bad
+    assert lib.spense_linear_w4a4(h.handle, ptr[0], 4, 64, ptr[2], sdg.DT_F32, 32, None) == unsupported
+    assert lib.spense_linear_w8a8(h.handle, ptr[0], 4, 64, ptr[2], sdg.DT_F32, 32, 0, None) == unsupported
+    assert lib.spense_export(h.handle, None, None, None, None, None, None) == bad
+    c, s = torch.zeros((32, 32), dtype=torch.uint8, device="cuda"), torch.zeros((32, 2), dtype=torch.uint8, device="cuda")
+    layer = sdg.SpenseLinearMx4(c, s)
+    assert call(handle=layer.handle) == bad
+    assert lib.spense_linear_noalloc(layer.handle, ptr[0], sdg.DT_BF16, 4, 64, ptr[2], sdg.DT_F32, 32, None) == unsupported
+    assert lib.spense_linear_splits(layer.handle, ptr[0], sdg.DT_BF16, 4, 64, ptr[2], sdg.DT_F32, 32, 2, None) == unsupported
+    assert lib.spense_linear(layer.handle, ptr[0], sdg.DT_F32, 4, 64, ptr[2], sdg.DT_F32, 32, None) == unsupported
+    assert lib.spense_linear(layer.handle, ptr[0], sdg.DT_BF16, 0, 64, ptr[2], sdg.DT_F32, 32, None) == bad
+    torch.cuda.synchronize()
+    assert (Y == 7.0).all()
+    info = h.info
+    assert (info["split"], info["N"], info["K"], info["N_s"], info["N_d"]) == (4, 32, 64, 2, 16)
