@@ -324,8 +324,10 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   };
 
   // ---- activations.  A copy takes four rows x 256 bytes: lane l row l / 16,
-  // piece (l % 16) ^ (row % 16) of 16 bytes, so that the lanes reading one
-  // piece of 16 rows hit different banks.  Rows past the group and bytes
+  // piece (l % 16) ^ ((row - 4) % 16) of 16 bytes.  A read of 16 bytes a lane
+  // serves 16 lanes at a time, rows 0-3 and 12-15 of one piece with rows 4-11 of
+  // the next lane group's: with that shift they hit different banks for both
+  // orders of the pieces (without it the bf16 x mx4 product reads at half rate).  Rows past the group and bytes
   // past the row take an offset beyond the resource and land as zeros. ----
   constexpr int kQ = 4 * T;                           // copies of a stage
   constexpr int kPer = D * kQ / NW;                   // copies of a buffer per wave
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
     return q < 0 || q >= a.M ? 0xFFFFFFFFu : (uint32_t)q;
   };
   const int q0 = kQ >= NW ? wave : wave % kQ;
-  const int cr = lane >> 4, piece = (lane & 15) ^ (4 * (q0 & 3) + cr);
+  const int cr = lane >> 4, piece = (lane & 15) ^ ((4 * (q0 & 3) + cr - 4) & 15);
   uint32_t xo[kRowsPer];
 #pragma unroll
   for (int i = 0; i < kRowsPer; ++i) {
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   const int fr = lane & 15;
   auto frag_off = [&](int i) __attribute__((always_inline)) -> uint32_t {
     const int pc = WK && !XK ? 4 * g + i : 4 * i + g;
-    return (uint32_t)(fr * kStageBytes + 16 * (pc ^ fr));
+    return (uint32_t)(fr * kStageBytes + 16 * (pc ^ ((fr - 4) & 15)));
   };
   uint32_t fo[4];
 #pragma unroll
