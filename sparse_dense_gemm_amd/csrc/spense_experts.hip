@@ -27,6 +27,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));  // at any element's address
 
 // Configurations: X(index, waves, row tiles per wave R, m-tiles T, stages D in
 // the ring and in an LDS buffer, waves per SIMD the registers allow)
@@ -161,7 +162,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 // `have` rows; col0: output column of the wave's first tile.
 template <int R>
 __device__ __forceinline__ void put_rows(const ExpertsDesc& d, const ExpertsArgs& a, const f32x4 (&v)[R], uint8_t* lds,
-                                         int64_t m0, int have, int64_t col0, bool wide) {
+                                         int64_t m0, int have, int64_t col0) {
   const int lane = threadIdx.x & 63, fr = lane & 15, g = lane >> 4;
   const int eb = a.ydtype == DT_F32 ? 4 : 2;
   const int cols = d.glu ? 8 * R : 16 * R;           // output columns of the block
@@ -189,8 +190,8 @@ __device__ __forceinline__ void put_rows(const ExpertsDesc& d, const ExpertsArgs
     if (m >= have || col >= N) continue;
     const uint8_t* from = lds + m * pitch + 16 * c;
     uint8_t* to = (uint8_t*)a.Y + ((m0 + m) * a.ldy + col) * eb;
-    if (wide && col + per <= N) {
-      *(u32x4*)to = *(const u32x4*)from;
+    if (col + per <= N) {
+      *(u32x4_any*)to = *(const u32x4*)from;
     } else {
       for (int k = 0; k < per && col + k < N; ++k) {
         if (eb == 4) ((uint32_t*)to)[k] = ((const uint32_t*)from)[k];
@@ -251,7 +252,7 @@ __device__ __forceinline__ void finish(const ExpertsDesc& d, const ExpertsArgs& 
         }
       }
     }
-    put_rows<R>(d, a, v, lds, row0 + 16 * t, cnt - 16 * t, rt0 * (d.glu ? 8 : 16), a.yvec);
+    put_rows<R>(d, a, v, lds, row0 + 16 * t, cnt - 16 * t, rt0 * (d.glu ? 8 : 16));
   }
 }
 
@@ -560,14 +561,19 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* X, int64_
   if (row >= R) return;
   const int64_t r = row, k = (int64_t)(id - row * per) * 8;
   const int64_t src = rows ? rows[r] : r;
-  uint16_t v[8];
+  const bool in = src >= 0 && src < M;
+  u32x4 o = u32x4{0, 0, 0, 0};
+  if (in && k + 8 <= K) {
+    o = *(const u32x4_any*)(X + src * ldx + k);
+  } else if (in) {
+    uint16_t v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = src >= 0 && src < M && k + i < K ? X[src * ldx + k + i] : (uint16_t)0;
-  u32x4 o;
-  o.x = v[0] | ((uint32_t)v[1] << 16);
-  o.y = v[2] | ((uint32_t)v[3] << 16);
-  o.z = v[4] | ((uint32_t)v[5] << 16);
-  o.w = v[6] | ((uint32_t)v[7] << 16);
+    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? X[src * ldx + k + i] : (uint16_t)0;
+    o.x = v[0] | ((uint32_t)v[1] << 16);
+    o.y = v[2] | ((uint32_t)v[3] << 16);
+    o.z = v[4] | ((uint32_t)v[5] << 16);
+    o.w = v[6] | ((uint32_t)v[7] << 16);
+  }
   *(u32x4*)(out + r * ldo + 2 * k) = o;
 }
 

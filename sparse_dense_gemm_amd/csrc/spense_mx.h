@@ -60,7 +60,6 @@ struct ExpertsArgs {
   void* Y;
   int64_t ldy;
   int32_t ydtype;
-  int32_t yvec;          // Y and its rows are 16-byte aligned
   float* ws;             // [splits][NT][R][16] partial sums (splits > 1)
   int32_t* counters;     // [m-tiles * row groups], zero between calls
 };

@@ -17,6 +17,11 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+// vectors at any address (global loads and stores take any alignment): rows of
+// odd lengths and matrices that start anywhere move at full width
+typedef u32x4 u32x4_any __attribute__((aligned(1)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
 
 // exponent byte of a block whose largest magnitude has the fp32 bits `m`
 __device__ __forceinline__ uint32_t block_exponent(uint32_t m) {
@@ -41,20 +46,19 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t e) {
   return c;
 }
 
-// eight values of row x from column k on, zeros from K on; `vec`: 16-byte
-// aligned rows whose length is a multiple of 8
+// eight values of row x from column k on, zeros from K on
 template <typename XT>
-__device__ __forceinline__ void load8(const XT* x, int64_t k, int64_t K, bool vec, float (&v)[8]) {
-  if (vec && k < K) {
+__device__ __forceinline__ void load8(const XT* x, int64_t k, int64_t K, float (&v)[8]) {
+  if (k + 8 <= K) {
     if constexpr (sizeof(XT) == 2) {
-      const u32x4 u = *(const u32x4*)(x + k);
+      const u32x4 u = *(const u32x4_any*)(x + k);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(u[i] << 16);
         v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
       }
     } else {
-      const f32x4 a = *(const f32x4*)(x + k), b = *(const f32x4*)(x + k + 4);
+      const f32x4 a = *(const f32x4_any*)(x + k), b = *(const f32x4_any*)(x + k + 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = a[i];
@@ -80,8 +84,7 @@ __device__ __forceinline__ void load8(const XT* x, int64_t k, int64_t K, bool ve
 template <typename XT, bool PACKED>
 __global__ __launch_bounds__(256) void quantize_kernel(const XT* X, int64_t M, int64_t K, int64_t ldx,
                                                        const int32_t* rows, int64_t R, uint8_t* codes, int64_t ldc,
-                                                       uint8_t* scales, int64_t lds, int64_t blocks, bool vec,
-                                                       bool cvec) {
+                                                       uint8_t* scales, int64_t lds, int64_t blocks) {
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;  // a launch has at most 2^30 threads
   const uint32_t b = id >> 2, brow = b / (uint32_t)blocks;
   const int64_t row = brow, col = b - brow * (uint32_t)blocks;
@@ -90,7 +93,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const XT* X, int64_t M, i
   const int64_t src = !in ? -1 : rows ? rows[row] : row;
   const int64_t k = col * kMxBlock + 8 * q;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (src >= 0 && src < M) load8<XT>(X + src * ldx, k, K, vec, v);
+  if (src >= 0 && src < M) load8<XT>(X + src * ldx, k, K, v);
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -111,8 +114,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(const XT* X, int64_t M, i
   } else {
     uint8_t* out = codes + row * ldc + col * 16 + 4 * q;
     const int64_t have = (K - k + 1) / 2;  // bytes of the row from here on
-    if (cvec && have >= 4) {
-      *(uint32_t*)out = c;
+    if (have >= 4) {
+      *(u32_any*)out = c;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -125,8 +128,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const XT* X, int64_t M, i
 // eight columns a thread
 template <typename YT>
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, int64_t ldc, const uint8_t* scales,
-                                                         int64_t lds, int64_t M, int64_t K, YT* Y, int64_t ldy,
-                                                         bool vec, bool cvec) {
+                                                         int64_t lds, int64_t M, int64_t K, YT* Y, int64_t ldy) {
   const uint32_t per = (uint32_t)((K + 7) / 8), id = blockIdx.x * 256u + threadIdx.x;
   const uint32_t r = id / per;
   const int64_t row = r, k = (int64_t)(id - r * per) * 8;
@@ -134,8 +136,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, i
   const uint8_t* in = codes + row * ldc + k / 2;
   uint32_t c = 0;
   const int64_t have = (K - k + 1) / 2;
-  if (cvec && have >= 4) {
-    c = *(const uint32_t*)in;
+  if (have >= 4) {
+    c = *(const u32_any*)in;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -150,8 +152,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, i
     w.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
     w.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
     w.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
-    if (vec) {
-      *(u32x4*)out = w;
+    if (k + 8 <= K) {
+      *(u32x4_any*)out = w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -163,9 +165,9 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, i
     p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
     p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
     p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
-    if (vec) {
-      *(f32x4*)out = f32x4{p[0].x, p[0].y, p[1].x, p[1].y};
-      *(f32x4*)(out + 4) = f32x4{p[2].x, p[2].y, p[3].x, p[3].y};
+    if (k + 8 <= K) {
+      *(f32x4_any*)out = f32x4{p[0].x, p[0].y, p[1].x, p[1].y};
+      *(f32x4_any*)(out + 4) = f32x4{p[2].x, p[2].y, p[3].x, p[3].y};
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -185,7 +187,7 @@ __device__ __forceinline__ int64_t packed_row(const ExpertsDesc& d, int64_t r) {
 // each, of row tiles t0 .. t0 + tiles - 1 counted over the experts.
 template <bool MX>
 __global__ __launch_bounds__(256) void pack_experts_kernel(ExpertsDesc d, int64_t t0, int64_t tiles, const uint8_t* W,
-                                                           int64_t ldw, bool vec) {
+                                                           int64_t ldw) {
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;  // a launch has at most 2^30 threads
   const int lane = (int)(id & 63);
   const uint32_t per = (uint32_t)(MX ? d.NU : 4 * d.NU);  // kilobytes of a row tile
@@ -205,8 +207,8 @@ __global__ __launch_bounds__(256) void pack_experts_kernel(ExpertsDesc d, int64_
     if constexpr (MX) {
       const int64_t k = (int64_t)u * kUnitK + 32 * g;
       const uint8_t* w = W + (e * d.N + src) * ldw + k / 2;
-      if (vec && k + 32 <= d.K) {
-        o.v = *(const u32x4*)w;
+      if (k + 32 <= d.K) {
+        o.v = *(const u32x4_any*)w;
       } else {
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -217,8 +219,8 @@ __global__ __launch_bounds__(256) void pack_experts_kernel(ExpertsDesc d, int64_
     } else {
       const int64_t k = (int64_t)u * 32 + 8 * g;
       const uint16_t* w = (const uint16_t*)W + (e * d.N + src) * ldw + k;
-      if (vec && k + 8 <= d.K) {
-        o.v = *(const u32x4*)w;
+      if (k + 8 <= d.K) {
+        o.v = *(const u32x4_any*)w;
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -250,8 +252,6 @@ __global__ __launch_bounds__(256) void pack_exponents_kernel(ExpertsDesc d, int6
   *(uint32_t*)(d.wpack + tile * d.tile_bytes + d.scale_off + (int64_t)i4 * 256 + lane * 4) = o;
 }
 
-bool aligned(const void* p, int64_t ld_bytes, int n) { return ((uintptr_t)p | (uintptr_t)ld_bytes) % n == 0; }
-
 unsigned groups(int64_t threads) { return (unsigned)((threads + 255) / 256); }
 
 // A launch's grid counts threads in 32 bits: f(first row, rows) over runs of
@@ -271,8 +271,6 @@ template <bool PACKED>
 hipError_t quantize(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t ldx, const int32_t* rows, int64_t R,
                     uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds, hipStream_t s) {
   const int64_t blocks = PACKED ? (mx_units(K) + 3) / 4 * 16 : (K + kMxBlock - 1) / kMxBlock;
-  const int eb = xdtype == DT_F32 ? 4 : 2;
-  const bool vec = aligned(X, ldx * eb, 16) && K % 8 == 0, cvec = aligned(codes, ldc, 4);
   return by_rows(R, blocks * 4, [&](int64_t r0, int64_t n) {
     // rows picked by index keep X's origin
     const int64_t x0 = rows ? 0 : r0 * ldx;
@@ -280,12 +278,10 @@ hipError_t quantize(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t
     const int64_t have = rows ? M : n;
     if (xdtype == DT_F32)
       quantize_kernel<float, PACKED><<<groups(n * blocks * 4), 256, 0, s>>>(
-          (const float*)X + x0, have, K, ldx, pick, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, blocks, vec,
-          cvec);
+          (const float*)X + x0, have, K, ldx, pick, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, blocks);
     else
       quantize_kernel<uint16_t, PACKED><<<groups(n * blocks * 4), 256, 0, s>>>(
-          (const uint16_t*)X + x0, have, K, ldx, pick, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, blocks, vec,
-          cvec);
+          (const uint16_t*)X + x0, have, K, ldx, pick, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, blocks);
   });
 }
 
@@ -304,14 +300,13 @@ hipError_t launch_mx4_activations(const void* X, int64_t M, int64_t K, int64_t l
 hipError_t launch_mx4_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t M,
                                  int64_t K, void* Y, int32_t ydtype, int64_t ldy, hipStream_t s) {
   const int64_t per = (K + 7) / 8;
-  const bool cvec = aligned(codes, ldc, 4), vec = aligned(Y, ldy * (ydtype == DT_F32 ? 4 : 2), 16) && K % 8 == 0;
   return by_rows(M, per, [&](int64_t r0, int64_t n) {
     if (ydtype == DT_F32)
       dequantize_kernel<float><<<groups(n * per), 256, 0, s>>>(codes + r0 * ldc, ldc, scales + r0 * lds, lds, n, K,
-                                                               (float*)Y + r0 * ldy, ldy, vec, cvec);
+                                                               (float*)Y + r0 * ldy, ldy);
     else
       dequantize_kernel<uint16_t><<<groups(n * per), 256, 0, s>>>(codes + r0 * ldc, ldc, scales + r0 * lds, lds, n, K,
-                                                                  (uint16_t*)Y + r0 * ldy, ldy, vec, cvec);
+                                                                  (uint16_t*)Y + r0 * ldy, ldy);
   });
 }
 
@@ -319,13 +314,12 @@ hipError_t launch_pack_experts(const ExpertsDesc& d, const void* W, int64_t ldw,
                                hipStream_t s) {
   const bool mx = d.wdtype == DT_MX4;
   const int64_t per = d.NU * (mx ? 64 : 256), per4 = (d.NU + 3) / 4 * 64;
-  const bool vec = aligned(W, mx ? ldw : 2 * ldw, 16);
   return by_rows(d.E * d.NT, per, [&](int64_t t0, int64_t n) {
     if (mx) {
-      pack_experts_kernel<true><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw, vec);
+      pack_experts_kernel<true><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw);
       pack_exponents_kernel<<<groups(n * per4), 256, 0, s>>>(d, t0, n, scales, lds);
     } else {
-      pack_experts_kernel<false><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw, vec);
+      pack_experts_kernel<false><<<groups(n * per), 256, 0, s>>>(d, t0, n, (const uint8_t*)W, ldw);
     }
   });
 }

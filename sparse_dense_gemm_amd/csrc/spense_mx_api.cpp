@@ -250,7 +250,6 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
   a.Y = Y;
   a.ldy = ldy;
   a.ydtype = ydtype;
-  a.yvec = ((uintptr_t)Y & 15) == 0 && ldy * (ydtype == SPENSE_F32 ? 4 : 2) % 16 == 0;
   // The product kernel reads rows of 16-byte pieces through offsets of 31
   // bits: mx4 activations are quantised into that form, bf16 ones are read in
   // place if they have it and laid out first if not.  Rows picked from beyond
