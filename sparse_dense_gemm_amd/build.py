@@ -25,7 +25,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-
 # The linear kernels rely on fully unrolled epilogue loops over register-
 # blocked accumulator tiles (up to 64 16x16 tiles per wave); above the default
 # size limit of a forced unroll the tile array would live in scratch memory.
-EXTRA = {f: ["-mllvm", "-pragma-unroll-threshold=200000"] 
+EXTRA = {f: ["-mllvm", "-pragma-unroll-threshold=200000"]
          for f in ("spense_kernels.hip", "spense_tile.hip", "spense_experts.hip")}
 
 

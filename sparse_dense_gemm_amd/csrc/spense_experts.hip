@@ -38,79 +38,107 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));  // at any element's addres
   X(3, 4, 2, 8, 1, 2)            \
   X(4, 4, 4, 8, 1, 2)
 
-// First of the 16 rows and expert of m-tile group j (groups of `rows` rows,
-// counted over the experts in order); cnt = 0 where there is no such group.
-__device__ __forceinline__ void find_group(const ExpertsDesc& d, const ExpertsArgs& a, int rows, int j, int& e,
-                                           int64_t& row0, int& cnt) {
-  if (!a.offsets) {
-    e = 0;
-    row0 = (int64_t)j * rows;
-    const int64_t left = a.R - row0;
-    cnt = (int)(left <= 0 ? 0 : left < rows ? left : rows);
-    return;
-  }
+// Groups of `rows` rows of the 64 experts from `base` on, lane i those of
+// expert base + i: their number, and the number of those before and with them
+// in this chunk; lo, hi: the expert's rows.
+__device__ __forceinline__ int chunk_groups(const ExpertsDesc& d, const ExpertsArgs& a, int rows, int64_t base, int& lo,
+                                            int& hi, int& incl) {
   const int lane = threadIdx.x & 63;
-  int before = 0;  // groups of the experts before this chunk of 64
-  e = 0;
-  row0 = 0;
-  cnt = 0;
-  for (int64_t base = 0; base < d.E; base += 64) {
-    const int64_t i = base + lane;
-    int64_t lo = 0, hi = 0;
-    if (i < d.E) {
-      lo = a.offsets[i];
-      hi = a.offsets[i + 1];
-      lo = lo < 0 ? 0 : lo > a.R ? a.R : lo;
-      hi = hi < lo ? lo : hi > a.R ? a.R : hi;
-    }
-    const int n = (int)((hi - lo + rows - 1) / rows);
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(incl, o);
-      if (lane >= o) incl += up;
-    }
-    const int excl = before + incl - n;
-    const uint64_t hit = __ballot(j >= excl && j < excl + n);
-    if (hit) {
-      const int src = __builtin_ctzll(hit);
-      const int k = j - __builtin_amdgcn_readlane(excl, src);
-      const int l0 = __builtin_amdgcn_readlane((int)lo, src), h0 = __builtin_amdgcn_readlane((int)hi, src);
-      e = (int)base + src;
-      row0 = (int64_t)l0 + (int64_t)k * rows;
-      const int left = h0 - (int)row0;
-      cnt = left < rows ? left : rows;
-      return;
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
+  const int64_t i = base + lane;
+  int64_t l = 0, h = 0;
+  if (i < d.E) {
+    l = a.offsets[i];
+    h = a.offsets[i + 1];
+    l = l < 0 ? 0 : l > a.R ? a.R : l;
+    h = h < l ? l : h > a.R ? a.R : h;
   }
+  lo = (int)l;
+  hi = (int)h;
+  const int n = (hi - lo + rows - 1) / rows;
+  incl = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(incl, o);
+    if (lane >= o) incl += up;
+  }
+  return n;
 }
 
-// Split, row group and m-tile group of this workgroup; false past the last.
-// Workgroups are dealt to the 8 XCDs round robin; the workgroups of an XCD take
-// the tiles in runs of p.run, so that those running together there form a
-// block of p.rblock row groups x some m-groups and share both operands in the
-// XCD's L2 (experts' gate/up, 16 x 3200 x 5120 bf16, 8192 rows: 2.3 GB of L2
-// misses without the runs).
-__device__ __forceinline__ bool tile_of(const ExpertsPlan& p, int& s, int& rg, int& j) {
-  const uint32_t b = blockIdx.x, xcd = b % 8u, seq = b / 8u;
-  const uint32_t run = (uint32_t)p.run, lap = seq / run;
+// Split, row group and m-group of this workgroup, of `groups` m-groups; false
+// past the last tile.  Workgroups are dealt to the 8 XCDs round robin; the
+// workgroups of an XCD take the tiles in runs, every XCD as many tiles, so that
+// those running together there form a block of p.rblock row groups x some
+// m-groups and share both operands in the XCD's L2 (gate/up of 8192 rows,
+// 3200 x 5120 bf16: blocks of 2 to 4 row groups 275 us, of 7 280, of 13 288).
+__device__ __forceinline__ bool tile_of(const ExpertsPlan& p, int groups, int& s, int& rg, int& j) {
+  const uint32_t per = (uint32_t)p.rgroups * (uint32_t)groups, all = per * (uint32_t)p.splits;
+  uint32_t run = (uint32_t)p.run;
+  if (run == 0) {
+    const uint32_t laps = (all + 511u) / 512u;
+    run = laps ? (all + 8u * laps - 1u) / (8u * laps) : 1u;
+  }
+  const uint32_t b = blockIdx.x, xcd = b % 8u, seq = b / 8u, lap = seq / run;
   uint32_t id = (lap * 8u + xcd) * run + (seq - lap * run);
-  const uint32_t per = (uint32_t)p.rgroups * (uint32_t)p.mgroups;
+  if (id >= all) return false;
   s = 0;
   if (p.splits > 1) {
     s = (int)(id / per);
     id -= (uint32_t)s * per;
   }
-  if (s >= p.splits || id >= per) return false;
   // blocks of rblock row groups (fewer in the last), one m-group after the other
-  const uint32_t span = (uint32_t)p.rblock * (uint32_t)p.mgroups;
+  const uint32_t span = (uint32_t)p.rblock * (uint32_t)groups;
   const uint32_t blk = id / span, r0 = blk * (uint32_t)p.rblock, rem = id - blk * span;
   const uint32_t left = (uint32_t)p.rgroups - r0, nb = left < (uint32_t)p.rblock ? left : (uint32_t)p.rblock;
   const uint32_t m = rem / nb;
   j = (int)m;
   rg = (int)(r0 + rem - m * nb);
   return true;
+}
+
+// This workgroup's tile: split s, row group rg, m-group j, which is `cnt` rows
+// of expert e from row0 on; false if it has none.  The m-groups are counted
+// over the experts in order, so only those that have rows are dealt to the XCDs
+// (dealing out every possible group left some XCDs with more of the real ones:
+// 13 tokens' rows of mx4 gate/up 22.6 us, now 18.7; 8192 rows of mx4 down with
+// its weighted sum 86.9, now 82.7).
+__device__ __forceinline__ bool find_tile(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPlan& p, int rows,
+                                          int& s, int& rg, int& j, int& e, int64_t& row0, int& cnt) {
+  if (!a.offsets) {
+    if (!tile_of(p, (int)((a.R + rows - 1) / rows), s, rg, j)) return false;
+    e = 0;
+    row0 = (int64_t)j * rows;
+    const int64_t left = a.R - row0;
+    cnt = (int)(left < rows ? left : rows);
+    return true;
+  }
+  int lo, hi, incl, groups = 0;
+  int n = chunk_groups(d, a, rows, 0, lo, hi, incl);
+  groups = __builtin_amdgcn_readlane(incl, 63);
+  for (int64_t base = 64; base < d.E; base += 64) {
+    chunk_groups(d, a, rows, base, lo, hi, incl);
+    groups += __builtin_amdgcn_readlane(incl, 63);
+  }
+  // offsets that are not in order can name rows twice; the counters hold p.mgroups
+  groups = groups < p.mgroups ? groups : p.mgroups;
+  if (!tile_of(p, groups, s, rg, j)) return false;
+  int before = 0;  // groups of the experts before this chunk of 64
+  for (int64_t base = 0; base < d.E; base += 64) {
+    if (d.E > 64) n = chunk_groups(d, a, rows, base, lo, hi, incl);
+    const int excl = before + incl - n;
+    const uint64_t hit = __ballot(j >= excl && j < excl + n);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      const int k = j - __builtin_amdgcn_readlane(excl, src);
+      const int l0 = __builtin_amdgcn_readlane(lo, src), h0 = __builtin_amdgcn_readlane(hi, src);
+      e = (int)base + src;
+      row0 = (int64_t)(l0 + k * rows);
+      const int left = h0 - (int)row0;
+      cnt = left < rows ? left : rows;
+      return cnt > 0;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
 }
 
 // exponent byte -> the power of two (255 -> NaN)
@@ -281,15 +309,15 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
 
   // ---- which tile ----
   const int S = p.splits;
-  int s, rg, j;
-  if (!tile_of(p, s, rg, j)) return;
-  int e, cnt;
+  int s, rg, j, e, cnt;
   int64_t row0;
-  find_group(d, a, kRows, j, e, row0, cnt);
+  if (!find_tile(d, a, p, kRows, s, rg, j, e, row0, cnt)) return;
+  s = __builtin_amdgcn_readfirstlane(s);
+  rg = __builtin_amdgcn_readfirstlane(rg);
+  j = __builtin_amdgcn_readfirstlane(j);
   e = __builtin_amdgcn_readfirstlane(e);
   cnt = __builtin_amdgcn_readfirstlane(cnt);
   row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)row0);
-  if (cnt <= 0) return;
   const int nst = (int)(XK ? (d.NU + 3) / 4 : d.NU);  // stages of K
   int lo, hi;
   split_range(nst, s, S, lo, hi);
@@ -526,11 +554,13 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   finish<R, T>(d, a, p, acc, xb + wave * kPartLds<R>, s, rg, j, rt0, row0, cnt, &last_flag);
 }
 
-// grid of a plan, 0 if it does not fit
+// grid of a plan, 0 if it does not fit: the workgroups of tile_of's runs for
+// the largest number of m-groups (fewer m-groups never take more)
 unsigned grid_of(const ExpertsDesc& d, const ExpertsPlan& p, int per, int threads) {
-  if (p.rgroups != (d.NT + per - 1) / per || p.run < 1 || p.rblock < 1) return 0;
+  if (p.rgroups != (d.NT + per - 1) / per || p.rblock < 1 || p.run < 0) return 0;
   const int64_t tiles = (int64_t)p.rgroups * p.mgroups * p.splits;
-  const int64_t grid = (tiles + 8 * p.run - 1) / (8 * p.run) * (8 * p.run);
+  const int64_t laps = (tiles + 511) / 512, run = p.run ? p.run : (tiles + 8 * laps - 1) / (8 * laps);
+  const int64_t grid = (tiles + 8 * run - 1) / (8 * run) * (8 * run);
   return grid < 1 || grid * threads > 0x7FFFFFFF ? 0u : (unsigned)grid;  // threads count in 32 bits
 }
 

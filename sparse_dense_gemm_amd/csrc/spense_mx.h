@@ -70,7 +70,7 @@ struct ExpertsPlan {
   int rgroups;  // groups of row tiles, one per workgroup
   int mgroups;  // groups of activation rows (upper bound over the experts)
   int rblock;   // row groups taken together before the next m-group (launch order)
-  int run;      // consecutive tiles that one XCD takes
+  int run;      // consecutive tiles that one XCD takes; 0: as many as gives every XCD the same
 };
 
 // A configuration of the product kernel: waves per workgroup, row tiles per

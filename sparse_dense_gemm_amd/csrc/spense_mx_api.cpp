@@ -118,19 +118,10 @@ ExpertsPlan make_plan(const ExpertsDesc& d, bool grouped, int64_t R, bool xmx) {
   const ExpertsShape c = experts_shape(p.config);
   // Launch order: large groups in blocks of four row groups, m-group by m-group
   // (the two workgroups of a CU, 32 apart, then share their row group's
-  // weights: experts' gate/up of 8192 rows 307 us, blocks of 13 row groups
-  // 339); small ones, whose weights are most of what is read, m-group by
-  // m-group of a single row group.  An XCD takes runs of consecutive tiles,
-  // every XCD as many: 64 at most, what runs on it together; grouped rows
-  // shorter ones, since the m-groups that no expert fills are the last of each
-  // block and would leave some XCDs with less (gate/up of 8192 rows: runs of 43
-  // 311 us, of 16 276 us).
-  p.rblock = c.t >= 8 ? (int)std::min(p.rgroups, 4) : 1;
-  if (f_rblock > 0) p.rblock = f_rblock;
-  const int64_t all = (int64_t)p.rgroups * p.mgroups * p.splits, laps = (all + 511) / 512;
-  p.run = (int)((all + 8 * laps - 1) / (8 * laps));
-  if (grouped) p.run = std::min(p.run, c.t >= 8 ? 16 : 8);
-  if (f_run > 0) p.run = f_run;
+  // weights), small ones, whose weights are most of what is read, m-group by
+  // m-group of a single row group.
+  p.rblock = f_rblock > 0 ? f_rblock : c.t >= 8 ? std::min(p.rgroups, 4) : 1;
+  p.run = f_run;
   return p;
 }
 
