@@ -300,7 +300,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   // first three quarters (in one go they hold up the LDS reads beside them),
   // and a stage's weights that come in one load are loaded a stage ahead.
   constexpr bool kSpread = D == 1, kAhead = kSpread && NL == 1;
-  constexpr int kYoung = kAhead ? 0 : kSpread ? 2 * R + (WK ? R : 0) : kWait;  // weight loads after the last copy
+  constexpr int kYoung = kAhead ? 0 : kSpread ? 2 * R : kWait;  // weight loads after the last copy
   __shared__ __attribute__((aligned(1024))) uint8_t xb[2 * kBuf];
   __shared__ int last_flag;
   const int lane = threadIdx.x & 63;
@@ -329,9 +329,8 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   const __amdgpu_buffer_rsrc_t wr =
       make_rsrc(d.wpack + ((int64_t)e * d.NT + (nrt ? rt0 : 0)) * d.tile_bytes, (uint32_t)(nrt * d.tile_bytes));
   const uint32_t tb = (uint32_t)d.tile_bytes, so = (uint32_t)d.scale_off;
-  constexpr int kSlots = kAhead ? 2 : D;
-  u32x4 w[kSlots][R][NL];
-  uint32_t sc[kSlots][WK ? R : 1];
+  u32x4 w[kAhead ? 2 : D][R][NL];
+  uint32_t sc[kSpread ? 2 : D][WK ? R : 1];
   auto load_w = [&](auto slot, int r, int i, int c) __attribute__((always_inline)) {
     const int st = lo + c;
     uint32_t off = (uint32_t)r * tb;
@@ -350,6 +349,11 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
       const uint32_t off = (uint32_t)r * tb + so + (uint32_t)(XK ? st : st >> 2) * 256u;
       sc[decltype(slot)::value][r] = buf_load4(wr, 4 * lane, c < n ? off : kOutOfRange);
     }
+  };
+
+  auto load_scales = [&](auto slot, int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_s(slot, r, c);
   };
 
   // ---- activations.  A copy takes four rows x 256 bytes: lane l row l / 16,
@@ -433,13 +437,15 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
 
   const uint32_t xlds = lds_addr(xb);
   copy_x(0, xlds);
+  // in the loop's order: the compiler's waits count the loads issued since
   static_for<0, D>([&](auto sl) __attribute__((always_inline)) {
+    if constexpr (kSpread) load_scales(sl, decltype(sl)::value);
+    static_for<0, NL>([&](auto ic) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      load_s(sl, r, decltype(sl)::value);
-#pragma unroll
-      for (int i = 0; i < NL; ++i) load_w(sl, r, i, decltype(sl)::value);
-    }
+      for (int r = 0; r < R; ++r) load_w(sl, r, decltype(ic)::value, decltype(sl)::value);
+    });
+    if constexpr (!kSpread) load_scales(sl, decltype(sl)::value);
+    __builtin_amdgcn_sched_barrier(0);
   });
   // Waits until this wave's copies have landed (at most `young` weight loads
   // are younger than they are) and its LDS reads are done, then for the others.
@@ -454,23 +460,16 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   for (int c0 = 0; c0 < n; c0 += D) {
     const uint32_t other = xlds + (kBuf - cur);
     if constexpr (!kSpread) {
-      if (c0 + D < n) copy_x(c0 + D, other);
+      copy_x(c0 + D, other);
     }
+    if constexpr (kSpread) load_scales(std::integral_constant<int, 1>{}, c0 + 1);
     if constexpr (kAhead) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        load_w(std::integral_constant<int, 1>{}, r, 0, c0 + 1);
-        load_s(std::integral_constant<int, 1>{}, r, c0 + 1);
-      }
+      for (int r = 0; r < R; ++r) load_w(std::integral_constant<int, 1>{}, r, 0, c0 + 1);
     }
-    bool done = false;
     static_for<0, D>([&](auto sl) __attribute__((always_inline)) {
       constexpr int i = decltype(sl)::value;
       const int c = c0 + i;
-      if (i > 0 && (done || c >= n)) {
-        done = true;
-        return;
-      }
       const uint8_t* xs = xb + cur + i * kStage;
       const uint8_t* xe = xb + cur + D * kStage + i * kScales;
       uint32_t sb[XK ? T : 1];
@@ -527,11 +526,11 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
             for (int r = 0; r < R; ++r) load_w(sl, r, q, c + D);
           }
           if constexpr (q == 3) {
+            if constexpr (NL == 1) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if constexpr (NL == 1) load_w(sl, r, 0, c + D);
-              load_s(sl, r, c + D);
+              for (int r = 0; r < R; ++r) load_w(sl, r, 0, c + D);
             }
+            if constexpr (!kSpread) load_scales(sl, c + D);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -539,10 +538,10 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
     });
     // the other buffer has landed and this one's reads are done
     ready(std::integral_constant<int, kYoung>{});
-    if constexpr (kAhead) {
+    if constexpr (kSpread && WK) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        w[0][r][0] = w[1][r][0];
+        if constexpr (kAhead) w[0][r][0] = w[1][r][0];
         sc[0][r] = sc[1][r];
       }
     }
