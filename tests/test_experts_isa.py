@@ -74,14 +74,15 @@ def test_copies_into_lds_have_landed_before_their_barrier(kernels):
     """The copies are assembly that the compiler does not count.  The wait before
     a barrier leaves at most as many loads in flight as were issued after the
     last copy (the counter retires in order), so every copy has landed; and
-    every copy has a wait state between it and the write of m0."""
+    every copy has the wait states that a scalar register written by a vector
+    instruction needs before it, which cover the one after a write of m0."""
     for name, lines in kernels.items():
         after, wait, barriers = None, None, 0
         for i, line in enumerate(lines):
             t = line.strip()
             if re.match(r"buffer_load_dword\S*\s.*\blds\b", t):
                 after = 0
-                assert lines[i - 1].strip() == "s_nop 0", name
+                assert lines[i - 1].strip() == "s_nop 4", name
             elif re.match(r"(global|buffer)_load", t) and after is not None:
                 after += 1
             w = re.search(r"s_waitcnt vmcnt\((\d+)\)", t)
