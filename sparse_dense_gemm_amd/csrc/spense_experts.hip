@@ -297,10 +297,12 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   constexpr int kWait = D * kLoads;                      // and of the whole ring
   static_assert(kWait < 64, "the wait fits the counter");
   // With one stage in the ring its copies are spread over the products of the
-  // first three quarters (in one go they hold up the LDS reads beside them),
-  // and a stage's weights that come in one load are loaded a stage ahead.
+  // first quarter (in one go they hold up the LDS reads beside them, 12288 x
+  // 5120 at 2048 rows 187 us instead of 181; over three quarters they land
+  // later, gate/up of 8192 rows 286 instead of 281), its exponent bytes are
+  // loaded a stage ahead, and so are weights that come in one load.
   constexpr bool kSpread = D == 1, kAhead = kSpread && NL == 1;
-  constexpr int kYoung = kAhead ? 0 : kSpread ? 2 * R : kWait;  // weight loads after the last copy
+  constexpr int kYoung = kAhead ? 0 : kSpread ? 4 * R : kWait;  // weight loads after the last copy
   __shared__ __attribute__((aligned(1024))) uint8_t xb[2 * kBuf];
   __shared__ int last_flag;
   const int lane = threadIdx.x & 63;
@@ -514,9 +516,9 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
 #pragma unroll
           for (int r = t * R / T; r < (t + 1) * R / T; ++r) widen(std::integral_constant<int, q + 1>{}, r);
         }
-        if constexpr (kSpread && k < 3 * T) {
+        if constexpr (kSpread && k < T) {
           // past the last stage they write zeros: no branch in the loop
-          static_for<k * kCopies / (3 * T), (k + 1) * kCopies / (3 * T)>(
+          static_for<k * kCopies / T, (k + 1) * kCopies / T>(
               [&](auto ic) __attribute__((always_inline)) { copy_one(c0 + D, other, ic); });
         }
         if constexpr (t == T - 1 && !kAhead) {
