@@ -15,7 +15,7 @@
 // wave streaming its own row tiles from memory through a ring of D stages in
 // registers (they are packed as the matrix instructions' operands, so they
 // need neither LDS nor a shuffle); activations are shared by the waves, so
-// they are copied into LDS, C stages at a time into one of two buffers while
+// they are copied into LDS, D stages at a time into one of two buffers while
 // the other is read.  A stage is 256 bytes of every row: 128 bf16 columns or
 // 512 mx4 columns, in both cases four operands of 16 bytes per lane.
 #include "spense_device.h"
@@ -29,6 +29,31 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));  // at any element's address
 
+// Per pair of operands a wave reads 16 bytes a lane of activations from LDS for
+// R products; per stage a workgroup takes R NW weight tiles and 16 T rows through
+// the CU's vector cache.  So large groups take the largest block whose sums fit
+// the registers of two workgroups per CU, 256 columns x 128 rows (R = 4, T = 8:
+// 128 registers): one workgroup's start, barriers and stores are then covered
+// by the other's products.  One workgroup of 256 x 256 halves the weights' bytes
+// and lost (55296 x 5120, 2048 rows, mx4 x mx4: 307 us, four waves of T = 16
+// 489, eight waves with both operands in LDS 324).  128 columns (R = 2) serve
+// where that leaves too few blocks.  Below 64 rows the weights' stream from
+// memory is all: more waves and a deeper ring, D stages of R row tiles in
+// flight per wave (25600 x 5120, one row: 13.2 us, 5.3 TB/s; 5120 x 25600, 32
+// rows: 20 us, 3.6 TB/s, its sums split six ways).
+//
+// What bounds the large ones (12288 x 5120 mx4 with bf16 rows 174-182 us, 1.45
+// PFLOP/s; 55296 x 5120 mx4 x mx4 297-309, 3.8; 16 experts of 3200 x 5120
+// bf16, 8192 rows, 268-280, 0.97 without padding): the matrix instructions are
+// busy in 67, 51 and 58% of the cycles, at a clock that the load brings down to
+// 1.6-2.0 GHz; the rest waits for operands (17, 29 and 26 bytes per cycle and CU
+// come from L2) and, in the second, for the stores.
+//
+// The compiler's waits for the weights count loads in order of issue, so loads
+// that were issued in another order before the loop, or only on some paths in it,
+// make it wait for the youngest: the first loads are in the loop's order, and
+// a pass has no branches (stages past the end load zeros).
+//
 // Configurations: X(index, waves, row tiles per wave R, m-tiles T, stages D in
 // the ring and in an LDS buffer, waves per SIMD the registers allow)
 #define SPENSE_EXPERT_CONFIGS(X) \
@@ -362,8 +387,9 @@ __global__ __launch_bounds__(NW * 64, WPS) void experts_kernel(ExpertsDesc d, Ex
   // piece (l % 16) ^ ((row - 4) % 16) of 16 bytes.  A read of 16 bytes a lane
   // serves 16 lanes at a time, rows 0-3 and 12-15 of one piece with rows 4-11 of
   // the next lane group's: with that shift they hit different banks for both
-  // orders of the pieces (without it the bf16 x mx4 product reads at half rate).  Rows past the group and bytes
-  // past the row take an offset beyond the resource and land as zeros. ----
+  // orders of the pieces (without it the bf16 x mx4 product reads at half
+  // rate).  Rows past the group and bytes past the row take an offset beyond the
+  // resource and land as zeros. ----
   constexpr int kQ = 4 * T;                           // copies of a stage
   constexpr int kPer = D * kQ / NW;                   // copies of a buffer per wave
   constexpr int kRowsPer = kQ >= NW ? kQ / NW : 1;    // different rows among them
@@ -584,7 +610,9 @@ hipError_t launch_t(const ExpertsDesc& d, const ExpertsArgs& a, const ExpertsPla
   }
 }
 
-// Rows of bf16 into rows of ldo bytes, columns from K on zero; eight columns a thread.
+// Rows of bf16 into rows of ldo bytes, columns from K on zero, for rows whose
+// length, stride or start is no whole number of 16 bytes, as the product's copies
+// need them.  Eight columns a thread; bound by memory.
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
                                                        const int32_t* rows, int64_t R, uint8_t* out, int64_t ldo) {
   const uint32_t per = (uint32_t)(ldo / 16), id = blockIdx.x * 256u + threadIdx.x;  // at most 2^30 threads

@@ -44,8 +44,8 @@ int status_of(hipError_t e) {
 // every activation row) a workgroup multiplies 4 waves r t operand pairs at 16
 // cycles on each of four SIMDs and moves its weights and activations through
 // the CU's vector cache at 64 bytes a cycle; the two hardly overlap (55296 x
-// 5120 at 2048 rows: products alone 210 us, with either operand's loads 260,
-// with both 310).  A stage takes at least the memory latency over the stages
+// 5120 at 2048 rows: products alone 217 us, with the weights' or the rows'
+// loads 261 and 247, with both 302).  A stage takes at least the memory latency over the stages
 // in flight, and the launch the time its weights take from memory.  Two
 // workgroups run together on a CU.  With split K every sum is written and read
 // once more, and a workgroup reads its tile's S sums by itself.
@@ -59,9 +59,14 @@ double plan_cycles(const ExpertsDesc& d, int config, int64_t S, double groups, i
   const double latency = c.stages > 1 ? 3000.0 / c.stages : mx && !xmx ? 2000.0 : 5000.0;
   const int64_t rg = (d.NT + c.waves * c.r - 1) / (c.waves * c.r);
   const int64_t stages = ((xmx ? (d.NU + 3) / 4 : d.NU) + S - 1) / S;
+  // a pass takes the ring's stages together; those past the end wait for nothing
+  const int64_t empty = (stages + c.stages - 1) / c.stages * c.stages - stages;
   const int64_t load = (int64_t)std::ceil((double)rg * groups * (double)S / kCUs);  // workgroups of the fullest CU
-  double t = (double)(load / 2) * std::max(2.0 * work, latency) + (load % 2 ? std::max(1.3 * work, latency) : 0.0);
-  t = std::max(t * (double)stages, (double)(hit * d.NT * d.tile_bytes) / 2600.0);
+  auto stage = [&](double w, double least) {
+    return (double)(load / 2) * std::max(2.0 * w, least) + (load % 2 ? std::max(1.3 * w, least) : 0.0);
+  };
+  double t = stage(work, latency) * (double)stages + stage(0.5 * work, 0.0) * (double)empty;
+  t = std::max(t, (double)(hit * d.NT * d.tile_bytes) / 2600.0);
   t += 3000.0 * (double)((load + 1) / 2);
   if (S > 1) {
     const double tile = 1024.0 * c.waves * c.r * c.t;  // bytes of a workgroup's sums

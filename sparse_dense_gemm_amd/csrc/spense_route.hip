@@ -82,7 +82,11 @@ constexpr int kHeld = 4096;  // choices of a block that are kept in LDS
 // The choices of TB tokens.  G lanes share a token, V logits each; choice j is
 // kept by lane j % G until the weights' sum is known.  With one block of tokens
 // (fused) it also writes offsets, rows and final places; otherwise the block's
-// counts and each choice's place within the block.
+// counts and each choice's place within the block.  It reads every logit once
+// and waits for little else than its own chain of k maxima: G lanes to a token
+// keep it short (row rotations, no LDS), the least G and V that cover the
+// experts leave no lane idle.  One token, 16 experts, 2 choices: 3.3 us; 8191
+// tokens, 128 experts, 8 choices: 7.3 us, then 6.8 us of place_kernel.
 template <int G, int V, int NT>
 __global__ __launch_bounds__(NT) void choose_kernel(RouteArgs a, int TB, int fused) {
   extern __shared__ uint32_t bits[];  // [E][TB / 32], then (fused) [E] first rows
