@@ -39,7 +39,10 @@
  *     sizes them for every batch size up to its own, whatever split count the
  *     planner picks there.  spense_linear_splits with a forced split count
  *     sizes them for that call only.  The calls record kernel launches only;
- *     the split-K hand-off counters are reset by the kernels.
+ *     the split-K hand-off counters are reset by the kernels.  Workspaces that
+ *     a captured call used stay allocated until spense_free, so its graph may
+ *     also be replayed after a call that needed larger ones; not after
+ *     spense_free.
  */
 #ifndef SPENSE_H
 #define SPENSE_H

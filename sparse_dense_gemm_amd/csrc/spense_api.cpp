@@ -17,6 +17,7 @@
 #include "../../include/spense.h"
 #include "spense_internal.h"
 #include "spense_mx.h"
+#include "spense_workspace.h"
 
 using namespace spense;
 
@@ -38,6 +39,7 @@ struct spense_layer {
   size_t xws_bytes = 0;
   int32_t* counters = nullptr;
   size_t n_counters = 0;
+  GraphKept<kWorkspaces> graphs;  // workspaces that captured calls hold
   int32_t* ycol = nullptr;  // output column of each packed row, -1 on padding rows
   int32_t* wrow = nullptr;  // W row of each packed row (parts of an output-split layer)
   int64_t weight_bytes = 0;
@@ -760,6 +762,7 @@ struct WsNeed {
     ws = std::max(ws, o.ws);
     cnt = std::max(cnt, o.cnt);
   }
+  bool any() const { return xws || ws || cnt; }
   bool fits(const spense_layer* h) const { return xws <= h->xws_bytes && ws <= h->ws_bytes && cnt <= h->n_counters; }
 };
 
@@ -791,15 +794,15 @@ static WsNeed large_batch_bound(const LayerDesc& d) {
 }
 
 // Replaces h's workspaces with ones of at least `need` (synchronising the
-// stream first: earlier launches may still use the old ones).  New counters
-// are cleared by a fill kernel on the stream.
+// stream first: earlier launches may still use the old ones; those that a graph
+// may hold stay).  New counters are cleared by a fill kernel on the stream.
 static int grow_workspaces(spense_layer* h, const WsNeed& need, hipStream_t s) {
   if (need.fits(h)) return SPENSE_OK;
   hipError_t e = hipStreamSynchronize(s);
   if (e != hipSuccess) return hip_fail(e);
-  auto regrow = [&](void** ptr, size_t& have, size_t want) -> int {
+  auto regrow = [&](int which, void** ptr, size_t& have, size_t want) -> int {
     if (want <= have) return SPENSE_OK;
-    if (*ptr) (void)hipFree(*ptr);
+    if (!h->graphs.drop(which, *ptr)) return SPENSE_ENOMEM;
     *ptr = nullptr;
     have = 0;
     const hipError_t err = hipMalloc(ptr, want);
@@ -807,11 +810,11 @@ static int grow_workspaces(spense_layer* h, const WsNeed& need, hipStream_t s) {
     have = want;
     return SPENSE_OK;
   };
-  int rc = regrow(&h->xws, h->xws_bytes, need.xws);
-  if (rc == SPENSE_OK) rc = regrow((void**)&h->ws, h->ws_bytes, need.ws);
+  int rc = regrow(kWsX, &h->xws, h->xws_bytes, need.xws);
+  if (rc == SPENSE_OK) rc = regrow(kWsPartials, (void**)&h->ws, h->ws_bytes, need.ws);
   if (rc == SPENSE_OK && need.cnt > h->n_counters) {
     size_t bytes = h->n_counters * 4;
-    rc = regrow((void**)&h->counters, bytes, need.cnt * 4);
+    rc = regrow(kWsCounters, (void**)&h->counters, bytes, need.cnt * 4);
     h->n_counters = bytes / 4;
     if (rc == SPENSE_OK) {
       e = launch_zero_i32(h->counters, (int64_t)need.cnt, s);
@@ -963,7 +966,10 @@ static int run_layers(spense_layer* const* parts, int n_parts, int64_t M, int32_
       for (int i = 0; i < n_parts; ++i)
         if ((rc = grow_workspaces(parts[i], need[i], s)) != SPENSE_OK) return rc;
     }
-    for (int i = 0; i < n_parts; ++i) w[i] = handle_ws(parts[i]);
+    for (int i = 0; i < n_parts; ++i) {
+      if (need[i].any()) parts[i]->graphs.used(s);
+      w[i] = handle_ws(parts[i]);
+    }
   }
   for (int i = 0; i < n_parts; ++i) {
     rc = bind_call(parts[i], M, p[i], aa[i], gather_now[i], w[i], s);
@@ -1115,6 +1121,7 @@ int spense_linear_w8a8(spense_handle h, const void* X, int64_t M, int64_t ldx, v
     }
     if ((rc = grow_workspaces(h, need, s)) != SPENSE_OK) return rc;
   }
+  h->graphs.used(s);
   // workspace: the codes [M][K_p] in X'p order, then the token scales [M]
   uint8_t* q = (uint8_t*)h->xws;
   float* sx = (float*)(q + a8_codes_bytes(M, d.K_p));

@@ -9,6 +9,7 @@
 
 #include "../../include/spense.h"
 #include "spense_mx.h"
+#include "spense_workspace.h"
 
 namespace spense {
 
@@ -23,6 +24,7 @@ struct ExpertsLayer {
   size_t ws_bytes = 0;
   int32_t* counters = nullptr;
   size_t n_counters = 0;
+  GraphKept<kWorkspaces> graphs;  // workspaces that captured calls hold
   // rows that ws and counters have been sized for, whatever split count a
   // smaller call's plan takes: [mx4 activations][grouped]
   int64_t sized[2][2] = {{0, 0}, {0, 0}};
@@ -153,13 +155,13 @@ bool fits(const ExpertsLayer* h, const Need& n) {
 }
 
 // Replaces the workspaces that are too small (earlier launches may still use
-// them, so the stream is synchronised first).
+// them, so the stream is synchronised first; those that a graph may hold stay).
 int grow(ExpertsLayer* h, const Need& n, hipStream_t s) {
   hipError_t e = hipStreamSynchronize(s);
   if (e != hipSuccess) return status_of(e);
-  auto regrow = [&](void** p, size_t& have, int64_t want) -> int {
+  auto regrow = [&](int which, void** p, size_t& have, int64_t want) -> int {
     if (want <= (int64_t)have) return SPENSE_OK;
-    if (*p) (void)hipFree(*p);
+    if (!h->graphs.drop(which, *p)) return SPENSE_ENOMEM;
     *p = nullptr;
     have = 0;
     const hipError_t err = hipMalloc(p, (size_t)want);
@@ -167,11 +169,11 @@ int grow(ExpertsLayer* h, const Need& n, hipStream_t s) {
     have = (size_t)want;
     return SPENSE_OK;
   };
-  int rc = regrow((void**)&h->xws, h->xws_bytes, n.xws);
-  if (rc == SPENSE_OK) rc = regrow((void**)&h->ws, h->ws_bytes, n.ws);
+  int rc = regrow(kWsX, (void**)&h->xws, h->xws_bytes, n.xws);
+  if (rc == SPENSE_OK) rc = regrow(kWsPartials, (void**)&h->ws, h->ws_bytes, n.ws);
   if (rc == SPENSE_OK && n.cnt > (int64_t)h->n_counters) {
     size_t bytes = h->n_counters * 4;
-    rc = regrow((void**)&h->counters, bytes, n.cnt * 4);
+    rc = regrow(kWsCounters, (void**)&h->counters, bytes, n.cnt * 4);
     h->n_counters = bytes / 4;
     if (rc == SPENSE_OK) {
       e = launch_zero_i32(h->counters, n.cnt, s);
@@ -280,6 +282,7 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
     if (rc != SPENSE_OK) return rc;
   }
   sized = std::max(sized, R);
+  if (need.xws || need.ws) h->graphs.used(s);
   hipError_t e = hipSuccess;
   a.M = M;
   if (prepare) {
