@@ -250,29 +250,27 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
   a.ydtype = ydtype;
   // The product kernel reads rows of 16-byte pieces through offsets of 31
   // bits: mx4 activations are quantised into that form, bf16 ones are read in
-  // place if they have it and laid out first if not.  Rows picked from beyond
-  // 31 bits are gathered by the same pass.
+  // place if they have it and laid out first if not: the R rows that are read,
+  // gathered if they are picked by index, or X's own if it has no more than R and
+  // lies within 31 bits.  So a call with fewer rows of X or in Y never needs a
+  // larger workspace.
   constexpr int64_t kSpan = int64_t(1) << 31;
   Need need = plan_need(d, p, R);
-  int64_t codes_bytes = 0, n_rows = M;
   bool prepare = true;
   if (xmx) {
     a.ldx = d.NU * 64;
     a.ldxs = (d.NU + 3) / 4 * 16;
     a.xbytes = a.ldx;
-    if (rows && M * a.ldx >= kSpan) n_rows = R;
-    codes_bytes = align256(n_rows * a.ldx);
-    need.xws = codes_bytes + n_rows * a.ldxs;
   } else {
     prepare = ((uintptr_t)X & 15) != 0 || ldx % 8 != 0 || d.K % 8 != 0 || 2 * ldx * 256 >= kSpan ||
               (rows && 2 * M * ldx >= kSpan);
     a.ldx = prepare ? (d.K + 7) / 8 * 16 : 2 * ldx;
     a.xbytes = (d.K + 7) / 8 * 16;
-    if (prepare) {
-      if (rows && M * a.ldx >= kSpan) n_rows = R;
-      need.xws = n_rows * a.ldx;
-    }
   }
+  const bool gather = rows && (R < M || M * a.ldx >= kSpan);
+  const int64_t n_rows = rows && !gather ? M : R;
+  const int64_t codes_bytes = xmx ? align256(n_rows * a.ldx) : 0;
+  if (prepare) need.xws = xmx ? codes_bytes + n_rows * a.ldxs : n_rows * a.ldx;
   int64_t& sized = h->sized[xmx][offsets != nullptr];
   if (R > sized) {  // every smaller call too: none of them may allocate later (graph capture)
     for (int64_t r = (sized / 16 + 1) * 16; r < R; r += 16) need.grow(plan_need(d, make_plan(d, offsets != nullptr, r, xmx), r));
@@ -286,7 +284,6 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
   hipError_t e = hipSuccess;
   a.M = M;
   if (prepare) {
-    const bool gather = n_rows != M || (rows && n_rows == R && M * a.ldx >= kSpan);
     const int32_t* pick = gather ? rows : nullptr;
     if (xmx) {
       a.xs = h->xws + codes_bytes;

@@ -107,3 +107,41 @@ def test_a_graph_keeps_only_what_it_recorded(lib):
     run(lib, h, 4000)
     assert grown <= lib.host_live_bytes() + kept
     lib.spense_free(h)
+
+
+MISALIGNED = P + 2
+LAYOUTS = {"mx4": (sdg.DT_MX4, P), "bf16": (sdg.DT_BF16, MISALIGNED)}  # calls that lay X out first
+
+
+def laid_out(lib, h, M, R, rows, form):
+    adtype, X = LAYOUTS[form]
+    lib.host_forget()
+    assert run_experts(lib, h, M, adtype, R, rows, X) == 0
+    return lib.host_seen(hl.LAID_OUT), lib.host_seen(hl.PICKED), lib.host_seen(hl.ALLOCATIONS)
+
+
+@pytest.mark.parametrize("form", LAYOUTS)
+def test_only_the_rows_that_are_read_are_laid_out(lib, form):
+    h = experts(lib)
+    assert laid_out(lib, h, 1000, 10, None, form)[:2] == (10, 0)       # grouped, the rest of X unused
+    assert laid_out(lib, h, 1000, 10, P, form)[:2] == (10, 1)          # a few picked rows
+    assert laid_out(lib, h, 10, 10, P, form)[:2] == (10, 0)
+    assert laid_out(lib, h, 10, 1000, P, form)[:2] == (10, 0)          # rows that repeat: each row of X once
+    assert laid_out(lib, h, 1 << 19, 1 << 20, P, form)[:2] == (1 << 20, 1)  # X past 31 bits
+    lib.spense_free(h)
+
+
+@pytest.mark.parametrize("form", LAYOUTS)
+@pytest.mark.parametrize("rows", [None, P], ids=["grouped", "picked"])
+@pytest.mark.parametrize("M,R", [(1 << 19, 6), ((1 << 19) + 5, 900), (700, 700), (90, 400), (1 << 19, (1 << 19) + 40)])
+def test_a_call_sizes_every_call_with_fewer_rows(lib, M, R, rows, form):
+    """After a call with M rows of X and R in Y none with fewer of either allocates (as a capture needs)."""
+    if rows is None and M < R:
+        pytest.skip("grouped rows of X are at least R")
+    h = experts(lib)
+    laid_out(lib, h, M, R, rows, form)
+    for m in (M - 1, M // 2, 1000, 600, 64, 1):
+        for r in (R, R - 1, R // 2, 500, 17, 1):
+            if 1 <= m <= M and 1 <= r <= R and (rows or m >= r):
+                assert laid_out(lib, h, m, r, rows, form)[2] == 0, (m, r)
+    lib.spense_free(h)
