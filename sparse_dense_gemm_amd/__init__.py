@@ -11,8 +11,9 @@ only to own device memory and to name the current HIP stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 
@@ -166,6 +167,32 @@ def dtype_of(t) -> int:
     if d is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
     return d
+
+
+def _need_dtype(t, dtype, what: str) -> None:
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} is {dtype}, not {t.dtype}")
+
+
+def _matrix(t, what: str):
+    """Rows, columns and row stride of a matrix that is contiguous along a row."""
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} {rows} x {cols} is not contiguous along a row")
+    return rows, cols, ld
+
+
+def _too_small(what: str, rows: int, cols: int):
+    raise ValueError(f"{what} does not hold {rows} rows of {cols} columns")
+
+
+def _need_flat(t, dtype, n: int, what: str) -> None:
+    """t is contiguous, of this type, and holds at least n values."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} is {dtype}, not {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what} {tuple(t.shape)} does not hold {n} contiguous values")
 
 
 def spense_pack(W, wdtype: Optional[int] = None, *, scales=None, dense_cols=None, dense_fraction: float = 0.0,
@@ -329,7 +356,8 @@ def spense_quantize_tokens(X, Xq, sx, *, M: Optional[int] = None, K: Optional[in
 
 def spense_linear_w8a8(h: int, X, Y, *, splits: int = 0, ydtype: Optional[int] = None, M: Optional[int] = None,
                        ldx: Optional[int] = None, ldy: Optional[int] = None, stream=None) -> None:
-    """Y = (per-token e4m3 X) . W^T on an e4m3 input-split layer (asynchronous on the stream)."""
+    """Y = (per-token e4m3 X) . W^T on an e4m3 input-split layer, X bfloat16 (asynchronous on the stream)."""
+    _need_dtype(X, _torch().bfloat16, "X")
     if ydtype is None:
         ydtype = dtype_of(Y)
     if M is None:
@@ -344,48 +372,91 @@ def spense_linear_w8a8(h: int, X, Y, *, splits: int = 0, ydtype: Optional[int] =
 
 def spense_quantize_mx4(X, codes, scales, *, xdtype: Optional[int] = None, stream=None) -> None:
     """mx4 form of X [M, K]: codes (uint8 [M, >= (K+1)/2]) and exponent bytes (uint8 [M, >= ceil(K/32)])."""
-    xdtype = dtype_of(X) if xdtype is None else xdtype
-    M, K = X.shape
-    _mx4_shape(codes, scales, M, K)
-    st = _lib().spense_quantize_mx4(X.data_ptr(), xdtype, M, K, X.stride(0), codes.data_ptr(), codes.stride(0),
-                                    scales.data_ptr(), scales.stride(0), _stream(stream))
+    if xdtype is None:
+        xdtype = dtype_of(X)
+    else:
+        _need_width(X, xdtype, "X")
+    M, K, ldx = _matrix(X, "X")
+    ldc, lds = _mx4_strides(codes, scales, M, K)
+    st = _lib().spense_quantize_mx4(X.data_ptr(), xdtype, M, K, ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds,
+                                    _stream(stream))
     _check(st, "spense_quantize_mx4")
 
 
 def spense_dequantize_mx4(codes, scales, Y, *, ydtype: Optional[int] = None, stream=None) -> None:
     """The numbers an mx4 matrix stands for, into Y [M, K] (float32 or bfloat16)."""
-    ydtype = dtype_of(Y) if ydtype is None else ydtype
-    M, K = Y.shape
-    _mx4_shape(codes, scales, M, K)
-    st = _lib().spense_dequantize_mx4(codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), M, K,
-                                      Y.data_ptr(), ydtype, Y.stride(0), _stream(stream))
+    if ydtype is None:
+        ydtype = dtype_of(Y)
+    else:
+        _need_width(Y, ydtype, "Y")
+    M, K, ldy = _matrix(Y, "Y")
+    ldc, lds = _mx4_strides(codes, scales, M, K)
+    st = _lib().spense_dequantize_mx4(codes.data_ptr(), ldc, scales.data_ptr(), lds, M, K, Y.data_ptr(), ydtype, ldy,
+                                      _stream(stream))
     _check(st, "spense_dequantize_mx4")
 
 
-def _mx4_shape(codes, scales, rows: int, K: int) -> None:
-    c, s = codes.shape, scales.shape
-    if c[0] < rows or s[0] < rows or c[1] < (K + 1) // 2 or s[1] < (K + 31) // 32:
-        raise ValueError(f"codes {tuple(c)} and scales {tuple(s)} do not hold {rows} x {K} mx4")
-    if codes.element_size() != 1 or scales.element_size() != 1 or codes.stride(1) != 1 or scales.stride(1) != 1:
-        raise ValueError("codes and scales are bytes, contiguous along a row")
+_WIDTH = {DT_F32: 4, DT_BF16: 2, DT_FP8: 1, DT_MX4: 1}
+
+
+def _need_width(t, dtype: int, what: str) -> None:
+    """A type named by the caller has the width of t's elements (types the library refuses are left to it)."""
+    if t.element_size() != _WIDTH.get(dtype, t.element_size()):
+        raise TypeError(f"{what} of {t.dtype} does not hold elements of type {dtype}")
+
+
+def _mx4_strides(codes, scales, rows: int, K: int):
+    """Row strides of an mx4 matrix of at least rows x K."""
+    crows, cbytes, ldc = _matrix(codes, "codes")
+    srows, sbytes, lds = _matrix(scales, "scales")
+    if crows < rows or srows < rows or cbytes < (K + 1) // 2 or sbytes < (K + 31) // 32:
+        raise ValueError(f"codes {crows} x {cbytes} and scales {srows} x {sbytes} do not hold {rows} x {K} mx4")
+    if codes.element_size() != 1 or scales.element_size() != 1:
+        raise ValueError("codes and scales are bytes")
+    return ldc, lds
 
 
 def spense_pack_mx4(codes, scales, *, N: Optional[int] = None, K: Optional[int] = None, stream=None) -> int:
     """Pack an mx4 weight matrix [N, K] (K: twice the code bytes of a row unless given); returns the handle."""
     N = codes.shape[0] if N is None else N
     K = 2 * codes.shape[1] if K is None else K
-    _mx4_shape(codes, scales, N, K)
+    ldc, lds = _mx4_strides(codes, scales, N, K)
     h = ctypes.c_void_p()
-    st = _lib().spense_pack_mx4(codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), N, K,
-                                _stream(stream), ctypes.byref(h))
+    st = _lib().spense_pack_mx4(codes.data_ptr(), ldc, scales.data_ptr(), lds, N, K, _stream(stream), ctypes.byref(h))
     _check(st, "spense_pack_mx4")
     return h.value
 
 
+class _Dims(NamedTuple):
+    """What the calls on an mx4 layer or on experts' layers check tensors against."""
+    K: int
+    columns: int  # of an output row
+    experts: int
+
+
+def _dims(h: int) -> Optional[_Dims]:
+    """None for a handle of another kind, which the library refuses."""
+    info = LayerInfo()
+    _check(_lib().spense_info(h, ctypes.byref(info)), "spense_info")
+    return _Dims(info.K, info.N_d, info.N_s) if info.split in (3, 4) else None
+
+
 def spense_linear_w4a4(h: int, X, Y, *, M: Optional[int] = None, stream=None) -> None:
-    """Y = mx4(X) . W^T on an mx4 layer (asynchronous on the stream)."""
-    st = _lib().spense_linear_w4a4(h, X.data_ptr(), X.shape[0] if M is None else M, X.stride(0), Y.data_ptr(),
-                                   dtype_of(Y), Y.stride(0), _stream(stream))
+    """Y = mx4(X) . W^T on an mx4 layer, X bfloat16 (asynchronous on the stream)."""
+    _linear_w4a4(h, _dims(h), X, Y, M, stream)
+
+
+def _linear_w4a4(h, dims, X, Y, M, stream):
+    _need_dtype(X, _torch().bfloat16, "X")
+    xrows, xcols, ldx = _matrix(X, "X")
+    yrows, ycols, ldy = _matrix(Y, "Y")
+    M = xrows if M is None else M
+    if dims:
+        if xrows < M or xcols < dims.K:
+            _too_small("X", M, dims.K)
+        if yrows < M or ycols < dims.columns:
+            _too_small("Y", M, dims.columns)
+    st = _lib().spense_linear_w4a4(h, X.data_ptr(), M, ldx, Y.data_ptr(), dtype_of(Y), ldy, _stream(stream))
     _check(st, "spense_linear_w4a4")
 
 
@@ -397,9 +468,12 @@ def spense_pack_experts(W, wdtype: Optional[int] = None, *, scales=None, K: Opti
     if K is None:
         K = 2 * W.shape[2] if wdtype == DT_MX4 else W.shape[2]
     W2 = _rows_in_line(W)
+    _need_width(W, wdtype, "W")
+    if wdtype == DT_BF16 and W.shape[2] < K:
+        _too_small("W", E * N, K)
     s2 = None if scales is None else _rows_in_line(scales)
     if wdtype == DT_MX4 and s2 is not None:
-        _mx4_shape(W2, s2, E * N, K)
+        _mx4_strides(W2, s2, E * N, K)
     h = ctypes.c_void_p()
     st = _lib().spense_pack_experts(W2.data_ptr(), wdtype, _ptr(s2), E, N, K, W2.stride(0),
                                     0 if s2 is None else s2.stride(0), int(glu), _stream(stream), ctypes.byref(h))
@@ -416,14 +490,36 @@ def _rows_in_line(t):
 
 def spense_experts_linear(h: int, X, offsets, Y, *, rows=None, adtype: int = DT_BF16, R: Optional[int] = None,
                           stream=None) -> None:
-    """Rows of X grouped by expert (offsets int32 [E + 1], rows int32 [R] if X is not grouped itself) into Y [R, ...]."""
-    R = Y.shape[0] if R is None else R
-    st = _lib().spense_experts_linear(h, X.data_ptr(), adtype, X.shape[0], X.stride(0),
-                                      None if rows is None else rows.data_ptr(), offsets.data_ptr(), R, Y.data_ptr(),
-                                      dtype_of(Y), Y.stride(0), _stream(stream))
+    """Rows of X (bfloat16) grouped by expert (offsets int32 [E + 1], rows int32 [R] if X is not grouped itself)
+    into Y [R, ...]."""
+    _experts_linear(h, _dims(h), X, offsets, Y, rows, adtype, R, stream)
+
+
+def _experts_linear(h, dims, X, offsets, Y, rows, adtype, R, stream):
+    torch = _torch()
+    i32 = torch.int32
+    if X.dtype is not torch.bfloat16:
+        _need_dtype(X, torch.bfloat16, "X")
+    M, xcols, ldx = _matrix(X, "X")
+    yrows, ycols, ldy = _matrix(Y, "Y")
+    if R is None:
+        R = yrows
+    if dims:
+        K, columns, experts = dims
+        if xcols < K:
+            _too_small("X", M, K)
+        if yrows < R or ycols < columns:
+            _too_small("Y", R, columns)
+        if offsets.dtype is not i32 or offsets.numel() <= experts or not offsets.is_contiguous():
+            _need_flat(offsets, i32, experts + 1, "offsets")
+    if rows is not None and (rows.dtype is not i32 or rows.numel() < R or not rows.is_contiguous()):
+        _need_flat(rows, i32, R, "rows")
+    st = _lib().spense_experts_linear(h, X.data_ptr(), adtype, M, ldx, None if rows is None else rows.data_ptr(),
+                                      offsets.data_ptr(), R, Y.data_ptr(), dtype_of(Y), ldy, _stream(stream))
     _check(st, "spense_experts_linear")
 
 
+@functools.lru_cache(maxsize=256)
 def spense_route_workspace(T: int, E: int, k: int) -> int:
     """Bytes of workspace spense_route needs."""
     n = _lib().spense_route_workspace(T, E, k)
@@ -436,25 +532,41 @@ def spense_route(logits, k: int, ids, weights, offsets, rows, pos, work=None, *,
                  stream=None) -> None:
     """Experts of every token (ids int32, weights float32 [T, k]) and the tokens grouped by expert
     (offsets int32 [E + 1], rows int32 [T * k], pos int32 [T, k])."""
-    T, E = logits.shape
-    if ids.numel() < T * k or weights.numel() < T * k or rows.numel() < T * k or pos.numel() < T * k \
-            or offsets.numel() < E + 1:
+    T, E, ldl = _matrix(logits, "logits")
+    n = T * k
+    if ids.numel() < n or weights.numel() < n or rows.numel() < n or pos.numel() < n or offsets.numel() < E + 1:
         raise ValueError("ids, weights, rows and pos hold T * k values, offsets E + 1")
     need = spense_route_workspace(T, E, k)
-    if need and (work is None or work.numel() * work.element_size() < need):
-        raise ValueError(f"spense_route needs {need} bytes of workspace")
-    st = _lib().spense_route(logits.data_ptr(), dtype_of(logits), T, E, logits.stride(0), k, int(renormalize),
+    if need and (work is None or work.numel() * work.element_size() < need or not work.is_contiguous()):
+        raise ValueError(f"spense_route needs {need} contiguous bytes of workspace")
+    torch = _torch()
+    i32 = torch.int32
+    if not (ids.dtype is i32 and pos.dtype is i32 and rows.dtype is i32 and offsets.dtype is i32
+            and weights.dtype is torch.float32 and ids.is_contiguous() and pos.is_contiguous()
+            and rows.is_contiguous() and offsets.is_contiguous() and weights.is_contiguous()):
+        for t, what in ((ids, "ids"), (pos, "pos"), (rows, "rows"), (offsets, "offsets")):
+            _need_flat(t, i32, 0, what)
+        _need_flat(weights, torch.float32, 0, "weights")
+    st = _lib().spense_route(logits.data_ptr(), dtype_of(logits), T, E, ldl, k, int(renormalize),
                              ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
                              None if work is None else work.data_ptr(), _stream(stream))
     _check(st, "spense_route")
 
 
 def spense_experts_combine(O, pos, weights, Y, *, stream=None) -> None:
-    """Y[t] = sum_j weights[t, j] O[pos[t, j]]."""
+    """Y[t] = sum_j weights[t, j] O[pos[t, j]] (pos int32, weights float32 [T, k])."""
+    torch = _torch()
     T, k = pos.shape
-    st = _lib().spense_experts_combine(O.data_ptr(), dtype_of(O), O.shape[0], O.stride(0), pos.data_ptr(),
-                                       weights.data_ptr(), T, k, Y.shape[1], Y.data_ptr(), dtype_of(Y), Y.stride(0),
-                                       _stream(stream))
+    R, ocols, ldo = _matrix(O, "O")
+    yrows, N, ldy = _matrix(Y, "Y")
+    if ocols < N:
+        _too_small("O", R, N)
+    if yrows < T:
+        _too_small("Y", T, N)
+    _need_flat(pos, torch.int32, 0, "pos")
+    _need_flat(weights, torch.float32, T * k, "weights")
+    st = _lib().spense_experts_combine(O.data_ptr(), dtype_of(O), R, ldo, pos.data_ptr(), weights.data_ptr(), T, k, N,
+                                       Y.data_ptr(), dtype_of(Y), ldy, _stream(stream))
     _check(st, "spense_experts_combine")
 
 
@@ -516,13 +628,20 @@ class SpenseLinearMx4(_Owned):
     def __init__(self, codes, scales, **kw):
         self.handle = spense_pack_mx4(codes, scales, **kw)
         self.info = spense_info(self.handle)
+        self._dims = _dims(self.handle)
 
     def __call__(self, X, Y, stream=None):
-        spense_linear(self.handle, X, Y, stream=stream)
+        M, xcols, ldx = _matrix(X, "X")
+        yrows, ycols, ldy = _matrix(Y, "Y")
+        if xcols < self._dims.K:
+            _too_small("X", M, self._dims.K)
+        if yrows < M or ycols < self._dims.columns:
+            _too_small("Y", M, self._dims.columns)
+        spense_linear(self.handle, X, Y, M=M, ldx=ldx, ldy=ldy, stream=stream)
         return Y
 
     def w4a4(self, X, Y, stream=None):
-        spense_linear_w4a4(self.handle, X, Y, stream=stream)
+        _linear_w4a4(self.handle, self._dims, X, Y, None, stream)
         return Y
 
 
@@ -532,7 +651,8 @@ class SpenseExperts(_Owned):
     def __init__(self, W, wdtype: Optional[int] = None, **kw):
         self.handle = spense_pack_experts(W, wdtype, **kw)
         self.info = spense_info(self.handle)
+        self._dims = _dims(self.handle)
 
     def __call__(self, X, offsets, Y, *, rows=None, adtype: int = DT_BF16, stream=None):
-        spense_experts_linear(self.handle, X, offsets, Y, rows=rows, adtype=adtype, stream=stream)
+        _experts_linear(self.handle, self._dims, X, offsets, Y, rows, adtype, None, stream)
         return Y

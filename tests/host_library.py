@@ -17,7 +17,7 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 X, PARTIALS, COUNTERS, X_ROWS, LAID_OUT, PICKED, ALLOCATIONS = range(7)
 
 
-def load(folder) -> ctypes.CDLL:
+def build(folder) -> str:
     gxx = shutil.which("g++")
     if gxx is None or not os.path.isdir(os.path.join(ROCM, "include", "hip")):
         pytest.skip("needs g++ and the HIP headers")
@@ -28,7 +28,11 @@ def load(folder) -> ctypes.CDLL:
     r = subprocess.run([gxx, "-std=c++17", "-O1", "-w", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-D__HIP_PLATFORM_AMD__",
                         f"-I{ROCM}/include", *src, "-o", out], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
-    lib = ctypes.CDLL(out)
+    return out
+
+
+def load(folder) -> ctypes.CDLL:
+    lib = ctypes.CDLL(build(folder))
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     lib.host_seen.restype = i64
     lib.host_live.argtypes = [i64]
