@@ -149,14 +149,14 @@ _dtypes = {}
 
 
 def _torch():
-    global _torch_module, _raw_stream
+    global _torch_module, _raw_stream, _dtypes
     if _torch_module is None:
         import torch
 
-        _torch_module = torch
+        # each name is bound once it is whole, the module last: another thread may look at any of them meanwhile
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _dtypes.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float8_e4m3fn: DT_FP8,
-                        torch.uint8: DT_FP8})
+        _dtypes = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float8_e4m3fn: DT_FP8, torch.uint8: DT_FP8}
+        _torch_module = torch
     return _torch_module
 
 
