@@ -25,6 +25,8 @@
  *     current at the call (hipMalloc / torch CUDA tensors).  "host pointer" is
  *     ordinary CPU memory.
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
+ *   - A size may be zero where its range says so; matrices and lists without
+ *     elements may then be NULL.
  *   - Matrices are row-major; leading dimensions are in elements.
  *   - A HIP runtime failure returns SPENSE_EHIP; spense_last_hip_error()
  *     then returns the hipError_t value.  Faults inside a kernel surface at the
@@ -467,7 +469,8 @@ int spense_route(const void* logits, int32_t ltype, int64_t T, int64_t E, int64_
  *   pos, weights  device pointers, [T, k] (from spense_route); a pos outside
  *            [0, R) adds nothing.
  *   Y        device pointer, [T, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16), ldy >= N.
- * Summed in fp32 in the order of j, rounded once.  Asynchronous on `stream`.
+ * 0 <= T, R <= 2^24, 1 <= k <= 1024, N >= 1.  Summed in fp32 in the order of j,
+ * rounded once.  Asynchronous on `stream`.
  */
 int spense_experts_combine(const void* O, int32_t otype, int64_t R, int64_t ldo, const int32_t* pos,
                            const float* weights, int64_t T, int32_t k, int64_t N, void* Y, int32_t ydtype, int64_t ldy,

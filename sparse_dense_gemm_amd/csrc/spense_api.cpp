@@ -1301,7 +1301,7 @@ int spense_free(spense_handle h) {
 
 int spense_quantize_mx4(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, int64_t ldc,
                         uint8_t* scales, int64_t lds, void* stream) {
-  if (!X || !codes || !scales || !mx4_matrix_ok(M, K, ldc, lds) || ldx < K) return SPENSE_EINVAL;
+  if (!mx4_matrix_ok(M, K, ldc, lds) || ldx < K || (M > 0 && (!X || !codes || !scales))) return SPENSE_EINVAL;
   if (xdtype != SPENSE_F32 && xdtype != SPENSE_BF16)
     return xdtype == SPENSE_FP8_E4M3 || xdtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
   if (M == 0) return SPENSE_OK;
@@ -1311,7 +1311,7 @@ int spense_quantize_mx4(const void* X, int32_t xdtype, int64_t M, int64_t K, int
 
 int spense_dequantize_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t M, int64_t K,
                           void* Y, int32_t ydtype, int64_t ldy, void* stream) {
-  if (!codes || !scales || !Y || !mx4_matrix_ok(M, K, ldc, lds) || ldy < K) return SPENSE_EINVAL;
+  if (!mx4_matrix_ok(M, K, ldc, lds) || ldy < K || (M > 0 && (!codes || !scales || !Y))) return SPENSE_EINVAL;
   if (ydtype != SPENSE_F32 && ydtype != SPENSE_BF16)
     return ydtype == SPENSE_FP8_E4M3 || ydtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
   if (M == 0) return SPENSE_OK;
@@ -1352,7 +1352,7 @@ int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, in
 
 int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_t M, int64_t ldx, const int32_t* rows,
                           const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, void* stream) {
-  if (!h || h->split != 4 || !X || !offsets || !Y) return SPENSE_EINVAL;
+  if (!h || h->split != 4 || !offsets || (R > 0 && (!X || !Y))) return SPENSE_EINVAL;
   const ExpertsDesc& d = experts_desc(h->experts);
   if (M < (R ? 1 : 0) || M > (int64_t(1) << 24) || R < 0 || R > (int64_t(1) << 24)) return SPENSE_EINVAL;
   if (!rows && M < R) return SPENSE_EINVAL;
@@ -1387,7 +1387,7 @@ int spense_route(const void* logits, int32_t ltype, int64_t T, int64_t E, int64_
 int spense_experts_combine(const void* O, int32_t otype, int64_t R, int64_t ldo, const int32_t* pos,
                            const float* weights, int64_t T, int32_t k, int64_t N, void* Y, int32_t ydtype, int64_t ldy,
                            void* stream) {
-  if (!O || !pos || !weights || !Y) return SPENSE_EINVAL;
+  if (T > 0 && ((R > 0 && !O) || !pos || !weights || !Y)) return SPENSE_EINVAL;
   if (T < 0 || T > (int64_t(1) << 24) || R < 0 || R > (int64_t(1) << 24) || k < 1 || k > kMaxExperts) return SPENSE_EINVAL;
   if (N < 1 || N >= kMaxLd || ldo < N || ldy < N) return SPENSE_EINVAL;
   for (const int32_t t : {otype, ydtype})

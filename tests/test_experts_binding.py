@@ -182,3 +182,22 @@ def test_w8a8_takes_bf16_only():
         with pytest.raises(TypeError):
             sdg.spense_linear_w8a8(h, bad, Y, stream=0)
     sdg.spense_free(h)
+
+
+def test_nothing_to_do():
+    """Calls without rows: torch's empty tensors have no address."""
+    c, s = torch.zeros((0, K // 2), dtype=U8), torch.zeros((0, K // 32), dtype=U8)
+    assert c.data_ptr() == 0
+    sdg.spense_quantize_mx4(torch.zeros((0, K)), c, s, stream=0)
+    sdg.spense_dequantize_mx4(c, s, torch.zeros((0, K), dtype=BF16), stream=0)
+    no_pairs, offsets = torch.zeros((0, k), dtype=I32), torch.zeros(E + 1, dtype=I32)
+    for X in (torch.zeros((0, K), dtype=BF16), torch.zeros((T, K), dtype=BF16)):
+        experts()(X, offsets, torch.zeros((0, N)), stream=0)
+        experts()(X, offsets, torch.zeros((0, N)), rows=torch.zeros(0, dtype=I32), stream=0)
+    sdg.spense_route(torch.zeros((0, E)), k, no_pairs, torch.zeros((0, k)), offsets, torch.zeros(0, dtype=I32),
+                     no_pairs, stream=0)
+    for O in (torch.zeros((0, N)), torch.zeros((R, N))):
+        sdg.spense_experts_combine(O, no_pairs, torch.zeros((0, k)), torch.zeros((0, N)), stream=0)
+    # tokens whose experts gave no rows
+    sdg.spense_experts_combine(torch.zeros((0, N)), torch.zeros((T, k), dtype=I32), torch.zeros((T, k)),
+                               torch.zeros((T, N)), stream=0)
