@@ -368,7 +368,8 @@ int spense_quantize_mx4(const void* X, int32_t xdtype, int64_t M, int64_t K, int
 
 /*
  * spense_dequantize_mx4 - the numbers an mx4 matrix stands for, into Y [M, ldy] of
- * ydtype (SPENSE_F32 or SPENSE_BF16; exact in both, down to the subnormals).
+ * ydtype (SPENSE_F32 or SPENSE_BF16; exact in both, down to the subnormals; 2^128
+ * and more, which only scale bytes 253 and 254 can give, become infinities).
  * Sizes as for spense_quantize_mx4.  Asynchronous on `stream`.
  */
 int spense_dequantize_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int64_t M, int64_t K,
@@ -379,7 +380,11 @@ int spense_dequantize_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scal
  *
  * spense_linear runs it on bf16 activations, Y = X . W^T, with every product
  * exact and the sum in fp32; spense_linear_w4a4 quantises the activations
- * first.  spense_info and spense_free accept the handle;
+ * first.  With bf16 activations a weight is taken as bfloat16, which holds every
+ * code at scale bytes up to 252 (the largest that spense_quantize_mx4 gives); at
+ * 253 and 254 a magnitude of 2^128 or more counts as an infinity.  So it does
+ * for mx4 experts.  spense_linear_w4a4 takes all of them as they are.
+ * spense_info and spense_free accept the handle;
  * spense_linear_splits with a forced split count and spense_linear_noalloc
  * return SPENSE_EUNSUPPORTED.  Synchronises `stream` before returning.
  */

@@ -171,7 +171,8 @@ __device__ __forceinline__ float exp_scale(uint32_t b) {
   return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
 }
 
-// eight e2m1 codes times a power of two, exact in bf16
+// eight e2m1 codes times a power of two, exact in bf16 (2^128 and more, which only
+// bytes 253 and 254 can give, become infinities)
 __device__ __forceinline__ bf16x8 mx4x8_to_bf16(uint32_t c, float s) {
   u32x4 w;
   w.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
