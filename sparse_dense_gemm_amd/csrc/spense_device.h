@@ -431,29 +431,33 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // that the compiler does not track them: it would otherwise wait for copies
 // into other stage buffers before LDS reads whenever more copies are in
 // flight than it follows one by one.  The kernel waits for them itself (a
-// counted s_waitcnt before each stage's barrier).  The compiler
-// adds no wait states for assembly, so they are in it: one between a write of
-// m0 and an LDS copy, five between a vector instruction that writes a scalar
-// register (a resource word brought back from a spill) and a memory
-// instruction that reads it.  They cost nothing measurable (55296 x 5120 at
-// 2048 rows: 311 us with one or five).  NT: non-temporal cache policy.
-template <bool NT>
+// counted s_waitcnt before each stage's barrier).  The compiler adds no wait
+// states for assembly, so they are in it: one between a write of m0 and an LDS
+// copy, five between a vector instruction that writes a scalar register (a
+// resource word brought back from a spill) and a memory instruction that reads
+// it.  NOPS = 4 gives all five, and costs the expert products nothing (55296 x
+// 5120 at 2048 rows: 311 us with one or five).  The LDS-staged kernels of the
+// sparse layers, whose resource words stay in scalar registers, take NOPS = 0
+// (55296 x 5120 e4m3 at 128 rows: 69.4 us, with NOPS = 4 71.5); that no vector
+// instruction writes one within five is checked in their emitted code.
+// NT: non-temporal cache policy.
+template <bool NT, int NOPS = 4>
 __device__ __forceinline__ void copy16(const i32x4& r, uint32_t lds, uint32_t voff, uint32_t soff) {
   if constexpr (NT)
-    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+    asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds), "n"(NOPS) : "memory");
   else
-    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+    asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds), "n"(NOPS) : "memory");
 }
-template <bool NT>
+template <bool NT, int NOPS = 4>
 __device__ __forceinline__ void copy4(const i32x4& r, uint32_t lds, uint32_t voff, uint32_t soff) {
   if constexpr (NT)
-    asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2 offen nt lds"
-                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+    asm volatile("s_nop %4\n\tbuffer_load_dword %0, %1, %2 offen nt lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds), "n"(NOPS) : "memory");
   else
-    asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds"
-                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+    asm volatile("s_nop %4\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds), "n"(NOPS) : "memory");
 }
 
 // f(integral_constant<A>), ..., f(integral_constant<B - 1>), in order

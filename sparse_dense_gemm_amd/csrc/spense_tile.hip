@@ -146,10 +146,10 @@ __global__ __launch_bounds__(WR * WM * 64) void linear_tile_kernel(LayerDesc d, 
       const int r = wave + NWV * iu;
       if constexpr (part < (int)(UB / 1024)) {
         const uint32_t uoff = in ? (uint32_t)r * tb + (sp ? s_unit0 : d_unit0) + (uint32_t)k * UB : kOutOfRange;
-        copy16<NTW>(wres, lds_addr(buf + r * RS + 1024 * part), 16 * lane, uoff + 1024u * part);
+        copy16<NTW, 0>(wres, lds_addr(buf + r * RS + 1024 * part), 16 * lane, uoff + 1024u * part);
       } else {
         const uint32_t ioff = in && sp ? (uint32_t)r * tb + s_idx0 + (uint32_t)k * 256u : kOutOfRange;
-        copy4<NTW>(wres, lds_addr(buf + r * RS + UB), 4 * lane, ioff);
+        copy4<NTW, 0>(wres, lds_addr(buf + r * RS + UB), 4 * lane, ioff);
       }
     } else {
       constexpr int jx = i - kWC, it = jx / S_::kXB, blk = jx % S_::kXB;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(WR * WM * 64) void linear_tile_kernel(LayerDesc d, 
       const uint32_t col = !in ? kOutOfRange : sp ? s_col + (uint32_t)(128 * XB) * k : d_col + (uint32_t)(64 * XB) * k;
       const uint32_t v = (uint32_t)t * xtile + (sp ? xl_s : xl_d);
       if constexpr (A8) {
-        copy16<false>(xres, lds_addr(xb + 1024 * blk), v + xhalf * blk, col);
+        copy16<false, 0>(xres, lds_addr(xb + 1024 * blk), v + xhalf * blk, col);
       } else {
         // blocks (step q, row half rh) at 2048 q + 1024 rh; a dense unit uses
         // its one 64-column step for both products: its second step's blocks
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(WR * WM * 64) void linear_tile_kernel(LayerDesc d, 
         // offsets)
         constexpr int q = blk & 1, rh = blk >> 1;
         const uint32_t cq = q == 0 || !in ? col : sp ? col + 128u : col;
-        copy16<false>(xres, lds_addr(xb + 2048 * q + 1024 * rh), v + xhalf * rh, cq);
+        copy16<false, 0>(xres, lds_addr(xb + 2048 * q + 1024 * rh), v + xhalf * rh, cq);
       }
     }
   };
