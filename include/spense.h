@@ -35,16 +35,18 @@
  *     be in flight on a handle at a time (its split-K and gather workspaces
  *     are shared).
  *   - spense_linear, spense_linear_w8a8, spense_linear_w4a4, spense_glu and
- *     spense_experts_linear may be captured in a HIP graph once an eager call on the same handle at a batch size of at least
- *     the captured one has run (automatic split counts): a call that has to
- *     grow the handle's workspaces synchronises the stream and allocates, and
- *     sizes them for every batch size up to its own, whatever split count the
- *     planner picks there.  spense_linear_splits with a forced split count
- *     sizes them for that call only.  The calls record kernel launches only;
- *     the split-K hand-off counters are reset by the kernels.  Workspaces that
- *     a captured call used stay allocated until spense_free, so its graph may
- *     also be replayed after a call that needed larger ones; not after
- *     spense_free.
+ *     spense_experts_linear may be captured in a HIP graph once an eager call
+ *     on the same handle has sized its workspaces: a call that has to grow them
+ *     synchronises the stream and allocates.  Sparse layers (automatic split
+ *     counts): a call at the captured batch size, or a larger one that had to
+ *     grow them, which sizes them for every batch size up to its own, whatever
+ *     split count the planner picks there (spense_linear_splits with a forced
+ *     split count sizes them for that call only).  mx4 and experts' layers: any
+ *     call of the same entry point with at least as many rows (see there).  The
+ *     calls record kernel launches only; the split-K hand-off counters are reset
+ *     by the kernels.  Workspaces that a captured call used stay allocated until
+ *     spense_free, so its graph may also be replayed after a call that needed
+ *     larger ones; not after spense_free.
  */
 #ifndef SPENSE_H
 #define SPENSE_H
@@ -397,7 +399,11 @@ int spense_pack_mx4(const uint8_t* codes, int64_t ldc, const uint8_t* scales, in
  * X [M, ldx] bf16 is quantised as spense_quantize_mx4 does, into the handle's
  * workspace; products are exact, the sum runs in fp32 in a fixed order.
  * Y [M, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16).  1 <= M <= 2^24.
- * Workspaces, asynchrony and graph capture as for spense_linear.
+ * Workspaces, asynchrony and graph capture as for spense_linear on such a layer:
+ * a captured call needs an eager one of the same entry point with M at least its
+ * own and, for spense_linear, with X aligned alike and ldx at least its own (rows
+ * that do not start at 16 bytes, or a K that is no multiple of 8, are laid out in
+ * the workspace first, and so are rows 2^22 or more elements apart).
  */
 int spense_linear_w4a4(spense_handle h, const void* X, int64_t M, int64_t ldx, void* Y, int32_t ydtype, int64_t ldy,
                        void* stream);
@@ -434,10 +440,12 @@ int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, in
  *   R        grouped rows that rows and Y have room for, 0 <= R <= 2^24.
  *   Y        device pointer, [R, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16), ldy >= N (I).
  * The sizes of the groups stay on the device.  Deterministic; workspaces,
- * asynchrony and graph capture as for spense_linear (R and M at most those of
- * the eager call, with the same adtype, rows given or not alike and X aligned
+ * asynchrony and graph capture as for spense_linear (R, M and ldx at most those
+ * of the eager call, with the same adtype, rows given or not alike and X aligned
  * alike: rows of X that do not start at 16 bytes, or a K that is no multiple of
- * 8, are laid out in the workspace first).
+ * 8, are laid out in the workspace first, and so are rows far apart or beyond 2
+ * GB: the rows that are read, or all of X if picked rows may repeat and it has
+ * no more than R).
  */
 int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_t M, int64_t ldx, const int32_t* rows,
                           const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, void* stream);

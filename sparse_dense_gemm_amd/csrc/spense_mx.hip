@@ -262,7 +262,8 @@ __global__ __launch_bounds__(256) void pack_exponents_kernel(ExpertsDesc d, int6
 unsigned groups(int64_t threads) { return (unsigned)((threads + 255) / 256); }
 
 // A launch's grid counts threads in 32 bits: f(first row, rows) over runs of
-// rows of at most 2^30 threads (a row takes at most 2^18).
+// rows of at most 2^30 threads (a row takes at most 2^18, a row tile of weights
+// in packing at most 2^21).
 template <typename F>
 hipError_t by_rows(int64_t rows, int64_t threads_per_row, F&& f) {
   const int64_t most = (int64_t(1) << 30) / threads_per_row;
