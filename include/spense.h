@@ -34,14 +34,15 @@
  *   - The library is not thread-safe per handle: at most one spense_linear may
  *     be in flight on a handle at a time (its split-K and gather workspaces
  *     are shared).
- *   - spense_linear, spense_linear_w8a8, spense_linear_w4a4, spense_glu and
- *     spense_experts_linear may be captured in a HIP graph once an eager call
+ *   - spense_linear, spense_linear_w8a8, spense_linear_w4a4, spense_linear_fp8b,
+ *     spense_glu, spense_experts_linear and spense_experts_linear_fp8b may be
+ *     captured in a HIP graph once an eager call
  *     on the same handle has sized its workspaces: a call that has to grow them
  *     synchronises the stream and allocates.  Sparse layers (automatic split
  *     counts): a call at the captured batch size, or a larger one that had to
  *     grow them, which sizes them for every batch size up to its own, whatever
  *     split count the planner picks there (spense_linear_splits with a forced
- *     split count sizes them for that call only).  mx4 and experts' layers: any
+ *     split count sizes them for that call only).  mx4, fp8b and experts' layers: any
  *     call of the same entry point with at least as many rows (see there).  The
  *     calls record kernel launches only; the split-K hand-off counters are reset
  *     by the kernels.  Workspaces that a captured call used stay allocated until
@@ -89,12 +90,13 @@ typedef struct spense_layer_info {
   int64_t device_bytes;   /* bytes of the device-resident packed form, padding included */
   int32_t split;          /* 0: input-split layer (spense_pack); 1: output-split (spense_pack_rows);
                              2: GLU block (spense_pack_glu); 3: mx4 layer (spense_pack_mx4);
-                             4: experts' layers (spense_pack_experts) */
+                             4: experts' layers (spense_pack_experts); 5: fp8b layer
+                             (spense_pack_fp8b); 6: fp8b experts (spense_pack_experts_fp8b) */
   int64_t N_s, N_d;       /* output-split: 2:4 rows / dense rows (input-split: N and 0); for an
                              output-split layer K_s = K when N_s > 0 and K_d = K when N_d > 0.
                              GLU block: N = K = H, N_s / N_d = 2:4 / dense intermediate indices,
                              K_s / K_d those of the down projection.
-                             mx4 layer, experts' layers: N, K of one expert, K_d = K, N_s = experts,
+                             mx4 and fp8b layers, experts' layers: N, K of one expert, K_d = K, N_s = experts,
                              N_d = output columns (N / 2 of a gate/up layer); weight_bytes of all */
 } spense_layer_info;
 
@@ -332,7 +334,7 @@ int spense_quantize_tokens(const void* X, int64_t M, int64_t K, int64_t ldx, uin
  *
  *   h      an input-split layer packed from SPENSE_FP8_E4M3 weights
  *          (SPENSE_EUNSUPPORTED for other weight types and for output-split
- *          layers and GLU blocks).
+ *          layers and GLU blocks), or a layer from spense_pack_fp8b (see there).
  *   X      device pointer, [M, ldx] bf16, finite values, ldx >= K.
  *   Y      device pointer, [M, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16 RNE), ldy >= N.
  *   splits split-K factor as for spense_linear_splits (0: automatic).
@@ -488,6 +490,147 @@ int spense_route(const void* logits, int32_t ltype, int64_t T, int64_t E, int64_
 int spense_experts_combine(const void* O, int32_t otype, int64_t R, int64_t ldo, const int32_t* pos,
                            const float* weights, int64_t T, int32_t k, int64_t N, void* Y, int32_t ydtype, int64_t ldy,
                            void* stream);
+
+/*
+ * Block-scaled 8-bit weights and activations (fp8b).
+ *
+ * An fp8b matrix of M rows and K columns, its blocks `rows` rows high, is
+ *   codes   [M, ldc] bytes, ldc >= K: e4m3fn codes;
+ *   scales  [ceil(M / rows), lds] float32, lds >= ceil(K / 128): element (m, k)
+ *           stands for code * scales[m / rows][k / 128].
+ * Weights have rows = 128, activations rows = 1.
+ *
+ * spense_quantize_fp8b - the fp8b matrix of X.
+ *
+ * Per block of rows x 128 (the last ones may be smaller):
+ *   scale = max |x| / 448 as an fp32 quotient, 1 where that is 0;
+ *   code  = the e4m3fn number nearest to the fp32 quotient x / scale, ties to
+ *           the even code, magnitudes above 448 to 448, the sign kept;
+ * a block that holds a NaN or an infinity has the scale NaN and codes 0.  Exact:
+ * the same bits as the formula.
+ *
+ *   X       device pointer, [M, ldx] of xdtype (SPENSE_F32 or SPENSE_BF16), ldx >= K.
+ *   rows    1 or 128.
+ * 0 <= M <= 2^24, 1 <= K <= 2^20.  Asynchronous on `stream`.
+ */
+int spense_quantize_fp8b(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t ldx, int32_t rows,
+                         uint8_t* codes, int64_t ldc, float* scales, int64_t lds, void* stream);
+
+/*
+ * spense_dequantize_fp8b - the numbers an fp8b matrix stands for, into Y [M, ldy]
+ * of ydtype (SPENSE_F32 or SPENSE_BF16): the product of code and scale, rounded
+ * to fp32 and then, for SPENSE_BF16, to bf16.  Sizes as for
+ * spense_quantize_fp8b.  Asynchronous on `stream`.
+ */
+int spense_dequantize_fp8b(const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds, int32_t rows,
+                           int64_t M, int64_t K, void* Y, int32_t ydtype, int64_t ldy, void* stream);
+
+/*
+ * spense_pack_fp8b - a linear layer with fp8b weights W[N,K], blocks of 128 x 128
+ * (once per weight).
+ *
+ *   Y[m, n] = sum_b sx[m][b] * sw[n / 128][b] * sum_(k in b) x[m][k] * w[n][k]
+ *
+ * over the blocks b of 128 columns.  spense_linear takes bf16 activations as they
+ * are (sx = 1), spense_linear_w8a8 (splits = 0) quantises them first as
+ * spense_quantize_fp8b with rows = 1 does, into the handle's workspace, and
+ * spense_linear_fp8b takes activations that are quantised already.  The inner sum
+ * runs in fp32 on exact products; the product of the two scales is rounded to
+ * fp32 and multiplied in with a fused multiply-add, block after block.  spense_info
+ * and spense_free accept the handle; spense_linear_splits with a forced split
+ * count and spense_linear_noalloc return SPENSE_EUNSUPPORTED.
+ * Synchronises `stream` before returning.
+ */
+int spense_pack_fp8b(const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds, int64_t N, int64_t K,
+                     void* stream, spense_handle* out);
+
+/*
+ * spense_linear_fp8b - a layer from spense_pack_fp8b on quantised activations.
+ *
+ *   codes, scales  device pointers, [M, ldc] e4m3 codes, ldc >= K, and [M, lds]
+ *            float32, lds >= ceil(K / 128), for example from spense_quantize_fp8b
+ *            or spense_block_norm.
+ *   Y        device pointer, [M, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16), ldy >= N.
+ * 1 <= M <= 2^24.  Deterministic; workspaces, asynchrony and graph capture as for
+ * spense_linear on such a layer: a captured call needs an eager one of the same
+ * entry point with M at least its own and activations aligned alike with row
+ * strides at least its own (rows of codes that do not start at 16 bytes, or a K
+ * that is no multiple of 16, and rows of bf16 that do not start at 16 bytes, or a
+ * K that is no multiple of 8, are laid out in the workspace first, and so are
+ * rows 2^22 or more elements apart).
+ */
+int spense_linear_fp8b(spense_handle h, const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds, int64_t M,
+                       void* Y, int32_t ydtype, int64_t ldy, void* stream);
+
+/*
+ * spense_pack_experts_fp8b - the linear layers of E experts with fp8b weights.
+ *
+ *   W        device pointer, the experts' matrices one after the other: [E*N, ldw] codes.
+ *   scales   device pointer, [E*B, lds] float32, B = ceil(N / 128) blocks of rows
+ *            to an expert; with glu 2 ceil(N/2 / 128): the gate's, then the up
+ *            projection's, each counted from its own first row.
+ *   glu      as for spense_pack_experts.
+ * 1 <= E <= 1024.  spense_experts_linear runs them, with adtype SPENSE_BF16, or
+ * SPENSE_FP8_E4M3 to quantise the activations in the call (rows = 1), and
+ * spense_experts_linear_fp8b.  Synchronises `stream` before returning.
+ */
+int spense_pack_experts_fp8b(const uint8_t* W, const float* scales, int64_t E, int64_t N, int64_t K, int64_t ldw,
+                             int64_t lds, int32_t glu, void* stream, spense_handle* out);
+
+/*
+ * spense_experts_linear_fp8b - spense_experts_linear on quantised activations:
+ * codes [M, ldc] and scales [M, lds] as for spense_linear_fp8b, for a handle from
+ * spense_pack_experts_fp8b.  The other arguments, their ranges, workspaces and
+ * graph capture as for spense_experts_linear.
+ */
+int spense_experts_linear_fp8b(spense_handle h, const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds,
+                               int64_t M, const int32_t* rows, const int32_t* offsets, int64_t R, void* Y,
+                               int32_t ydtype, int64_t ldy, void* stream);
+
+/*
+ * spense_block_norm - the pass over the rows between two blocks of a decoder: the
+ * norm after a block, its gate, the scaled residual and the norm before the next.
+ *
+ *   o[t]  = O[t], or sum_j weights[t, j] O[pos[t, j]] (the experts' outputs, as
+ *           spense_experts_combine adds them)
+ *   b[t]  = post ? rms(o[t]) * post : o[t]          rms(v) = v / sqrt(mean(v^2) + eps)
+ *   r[t]  = scale * residual[t] + gate[t] * b[t]
+ *   y[t]  = rms(r[t]) * pre
+ *
+ * in fp32 throughout; r is rounded once into residual_out, y once into Y, from the
+ * unrounded r.
+ */
+typedef struct spense_norm {
+  int64_t T, H;              /* rows and columns: 0 <= T <= 2^24, 1 <= H <= 2^20 */
+  const void* O;             /* device pointer, [T, ldo] of otype; with pos [O_rows, ldo] */
+  int64_t ldo, O_rows;       /* 0 <= O_rows <= 2^24 */
+  const int32_t* pos;        /* device pointers, [T, k], or both NULL; a pos outside [0, O_rows) adds nothing */
+  const float* weights;
+  const void* post;          /* device pointer, [H] of wtype, or NULL: no norm after the block */
+  const void* pre;           /* device pointer, [H] of wtype, or NULL: ones */
+  const void* gate;          /* device pointer, [T, ldg] of gtype, or NULL: ones */
+  int64_t ldg;               /* 0: one row of gates for all */
+  const void* residual;      /* device pointer, [T, ldr] of rtype, or NULL: zeros */
+  int64_t ldr;
+  void* residual_out;        /* device pointer, [T, ldro] of rtype, may be residual itself (ldro == ldr); or NULL */
+  int64_t ldro;
+  void* Y;                   /* device pointer, [T, ldy] of ytype, or NULL; not both Y and residual_out NULL */
+  int64_t ldy;
+  float* yscales;            /* device pointer, [T, lds], with ytype SPENSE_FP8_E4M3: Y holds the codes and this
+                                the scales of spense_quantize_fp8b (rows = 1) of y; NULL for other types */
+  int64_t lds;
+  int32_t k;                 /* with pos: 1 <= k <= 1024 */
+  int32_t otype, wtype, gtype, rtype; /* SPENSE_F32 or SPENSE_BF16 */
+  int32_t ytype;             /* SPENSE_F32, SPENSE_BF16 or SPENSE_FP8_E4M3 */
+  float scale, eps;          /* finite scale; eps > 0 */
+} spense_norm;
+
+/*
+ * One launch, asynchronous on `stream`, graph-capturable, no state kept.  Besides
+ * residual_out as residual, no output may overlap an input or another output.
+ * Types of operands that are NULL are ignored.  Deterministic.
+ */
+int spense_block_norm(const spense_norm* n, void* stream);
 
 /* spense_info - sizes of a packed layer (host-side, no synchronisation). */
 int spense_info(spense_handle h, spense_layer_info* info);

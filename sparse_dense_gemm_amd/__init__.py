@@ -44,6 +44,21 @@ class SpenseError(RuntimeError):
         self.status = status
 
 
+class NormCall(ctypes.Structure):
+    """spense_norm of the C interface."""
+
+    _fields_ = [
+        ("T", ctypes.c_int64), ("H", ctypes.c_int64), ("O", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+        ("O_rows", ctypes.c_int64), ("pos", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+        ("post", ctypes.c_void_p), ("pre", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("residual_out", ctypes.c_void_p),
+        ("ldro", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("yscales", ctypes.c_void_p),
+        ("lds", ctypes.c_int64), ("k", ctypes.c_int32), ("otype", ctypes.c_int32), ("wtype", ctypes.c_int32),
+        ("gtype", ctypes.c_int32), ("rtype", ctypes.c_int32), ("ytype", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
 class LayerInfo(ctypes.Structure):
     _fields_ = [
         ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("K_s", ctypes.c_int64), ("K_d", ctypes.c_int64),
@@ -103,6 +118,20 @@ def _lib():
     lib.spense_route.restype = ctypes.c_int
     lib.spense_experts_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i32, i64, vp]
     lib.spense_experts_combine.restype = ctypes.c_int
+    lib.spense_quantize_fp8b.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, i64, vp]
+    lib.spense_quantize_fp8b.restype = ctypes.c_int
+    lib.spense_dequantize_fp8b.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, vp]
+    lib.spense_dequantize_fp8b.restype = ctypes.c_int
+    lib.spense_pack_fp8b.argtypes = [vp, i64, vp, i64, i64, i64, vp, ctypes.POINTER(vp)]
+    lib.spense_pack_fp8b.restype = ctypes.c_int
+    lib.spense_linear_fp8b.argtypes = [vp, vp, i64, vp, i64, i64, vp, i32, i64, vp]
+    lib.spense_linear_fp8b.restype = ctypes.c_int
+    lib.spense_pack_experts_fp8b.argtypes = [vp, vp, i64, i64, i64, i64, i64, i32, vp, ctypes.POINTER(vp)]
+    lib.spense_pack_experts_fp8b.restype = ctypes.c_int
+    lib.spense_experts_linear_fp8b.argtypes = [vp, vp, i64, vp, i64, i64, vp, vp, i64, vp, i32, i64, vp]
+    lib.spense_experts_linear_fp8b.restype = ctypes.c_int
+    lib.spense_block_norm.argtypes = [ctypes.POINTER(NormCall), vp]
+    lib.spense_block_norm.restype = ctypes.c_int
     lib.spense_info.argtypes = [vp, ctypes.POINTER(LayerInfo)]
     lib.spense_info.restype = ctypes.c_int
     lib.spense_export.argtypes = [vp, vp, vp, vp, vp, vp, vp]
@@ -356,7 +385,8 @@ def spense_quantize_tokens(X, Xq, sx, *, M: Optional[int] = None, K: Optional[in
 
 def spense_linear_w8a8(h: int, X, Y, *, splits: int = 0, ydtype: Optional[int] = None, M: Optional[int] = None,
                        ldx: Optional[int] = None, ldy: Optional[int] = None, stream=None) -> None:
-    """Y = (per-token e4m3 X) . W^T on an e4m3 input-split layer, X bfloat16 (asynchronous on the stream)."""
+    """Y = (per-token e4m3 X) . W^T on an e4m3 input-split layer, or (fp8b X) . W^T on an fp8b layer; X bfloat16
+    (asynchronous on the stream)."""
     _need_dtype(X, _torch().bfloat16, "X")
     if ydtype is None:
         ydtype = dtype_of(Y)
@@ -428,7 +458,7 @@ def spense_pack_mx4(codes, scales, *, N: Optional[int] = None, K: Optional[int] 
 
 
 class _Dims(NamedTuple):
-    """What the calls on an mx4 layer or on experts' layers check tensors against."""
+    """What the calls on an mx4 or fp8b layer or on experts' layers check tensors against."""
     K: int
     columns: int  # of an output row
     experts: int
@@ -438,7 +468,7 @@ def _dims(h: int) -> Optional[_Dims]:
     """None for a handle of another kind, which the library refuses."""
     info = LayerInfo()
     _check(_lib().spense_info(h, ctypes.byref(info)), "spense_info")
-    return _Dims(info.K, info.N_d, info.N_s) if info.split in (3, 4) else None
+    return _Dims(info.K, info.N_d, info.N_s) if info.split in (3, 4, 5, 6) else None
 
 
 def spense_linear_w4a4(h: int, X, Y, *, M: Optional[int] = None, stream=None) -> None:
@@ -570,6 +600,184 @@ def spense_experts_combine(O, pos, weights, Y, *, stream=None) -> None:
     _check(st, "spense_experts_combine")
 
 
+FP8B_BLOCK = 128
+
+
+def _need_codes(t, what: str) -> None:
+    if t.element_size() != 1:
+        raise TypeError(f"{what} are bytes (uint8 or float8_e4m3fn), not {t.dtype}")
+
+
+def _fp8b_strides(codes, scales, M: int, K: int, rows: int):
+    """Row strides of an fp8b matrix of at least M x K, its blocks `rows` rows high."""
+    crows, ccols, ldc = _matrix(codes, "codes")
+    srows, scols, lds = _matrix(scales, "scales")
+    _need_codes(codes, "codes")
+    if scales.dtype is not _torch().float32:
+        _need_dtype(scales, _torch().float32, "scales")
+    if crows < M or ccols < K or srows < -(-M // rows) or scols < -(-K // FP8B_BLOCK):
+        raise ValueError(f"codes {crows} x {ccols} and scales {srows} x {scols} do not hold {M} x {K} fp8b")
+    return ldc, lds
+
+
+def spense_quantize_fp8b(X, codes, scales, *, rows: int = 1, xdtype: Optional[int] = None, stream=None) -> None:
+    """fp8b form of X [M, K] in blocks of rows x 128 (rows: 1 or 128): codes (bytes [M, >= K]) and scales (float32
+    [ceil(M / rows), >= ceil(K / 128)])."""
+    if xdtype is None:
+        xdtype = dtype_of(X)
+    else:
+        _need_width(X, xdtype, "X")
+    M, K, ldx = _matrix(X, "X")
+    ldc, lds = _fp8b_strides(codes, scales, M, K, max(1, rows))
+    st = _lib().spense_quantize_fp8b(X.data_ptr(), xdtype, M, K, ldx, rows, codes.data_ptr(), ldc, scales.data_ptr(),
+                                     lds, _stream(stream))
+    _check(st, "spense_quantize_fp8b")
+
+
+def spense_dequantize_fp8b(codes, scales, Y, *, rows: int = 1, ydtype: Optional[int] = None, stream=None) -> None:
+    """The numbers an fp8b matrix stands for, into Y [M, K] (float32 or bfloat16)."""
+    if ydtype is None:
+        ydtype = dtype_of(Y)
+    else:
+        _need_width(Y, ydtype, "Y")
+    M, K, ldy = _matrix(Y, "Y")
+    ldc, lds = _fp8b_strides(codes, scales, M, K, max(1, rows))
+    st = _lib().spense_dequantize_fp8b(codes.data_ptr(), ldc, scales.data_ptr(), lds, rows, M, K, Y.data_ptr(), ydtype,
+                                       ldy, _stream(stream))
+    _check(st, "spense_dequantize_fp8b")
+
+
+def spense_pack_fp8b(codes, scales, *, N: Optional[int] = None, K: Optional[int] = None, stream=None) -> int:
+    """Pack an fp8b weight matrix [N, K] with scales of 128 x 128 blocks; returns the handle."""
+    N = codes.shape[0] if N is None else N
+    K = codes.shape[1] if K is None else K
+    ldc, lds = _fp8b_strides(codes, scales, N, K, FP8B_BLOCK)
+    h = ctypes.c_void_p()
+    st = _lib().spense_pack_fp8b(codes.data_ptr(), ldc, scales.data_ptr(), lds, N, K, _stream(stream), ctypes.byref(h))
+    _check(st, "spense_pack_fp8b")
+    return h.value
+
+
+def spense_linear_fp8b(h: int, codes, scales, Y, *, M: Optional[int] = None, stream=None) -> None:
+    """Y = X . W^T on an fp8b layer, X the codes (bytes [M, K]) and scales (float32 [M, ceil(K / 128)])."""
+    _linear_fp8b(h, _dims(h), codes, scales, Y, M, stream)
+
+
+def _linear_fp8b(h, dims, codes, scales, Y, M, stream):
+    M = codes.shape[0] if M is None else M
+    yrows, ycols, ldy = _matrix(Y, "Y")
+    if dims and (yrows < M or ycols < dims.columns):
+        _too_small("Y", M, dims.columns)
+    ldc, lds = _fp8b_strides(codes, scales, M, dims.K if dims else codes.shape[1], 1)
+    st = _lib().spense_linear_fp8b(h, codes.data_ptr(), ldc, scales.data_ptr(), lds, M, Y.data_ptr(), dtype_of(Y), ldy,
+                                   _stream(stream))
+    _check(st, "spense_linear_fp8b")
+
+
+def spense_pack_experts_fp8b(W, scales, *, K: Optional[int] = None, glu: bool = False, stream=None) -> int:
+    """Pack experts' fp8b weights: codes [E, N, K] and scales [E, B, ceil(K / 128)], B = ceil(N / 128) blocks of rows;
+    with glu 2 ceil(N/2 / 128), the gate's first."""
+    E, N = W.shape[0], W.shape[1]
+    K = W.shape[2] if K is None else K
+    W2, s2 = _rows_in_line(W), _rows_in_line(scales)
+    blocks = 2 * -(-(N // 2) // FP8B_BLOCK) if glu else -(-N // FP8B_BLOCK)
+    if scales.shape[0] != E or scales.shape[1] != blocks:
+        raise ValueError(f"scales {tuple(scales.shape)} are not {E} x {blocks} rows of blocks")
+    ldw, lds = _fp8b_strides(W2, s2, E * N, K, E * N)
+    h = ctypes.c_void_p()
+    st = _lib().spense_pack_experts_fp8b(W2.data_ptr(), s2.data_ptr(), E, N, K, ldw, lds, int(glu), _stream(stream),
+                                         ctypes.byref(h))
+    _check(st, "spense_pack_experts_fp8b")
+    return h.value
+
+
+def spense_experts_linear_fp8b(h: int, codes, scales, offsets, Y, *, rows=None, R: Optional[int] = None,
+                               stream=None) -> None:
+    """spense_experts_linear on quantised activations: codes (bytes [M, K]) and scales (float32 [M, ceil(K / 128)])."""
+    _experts_linear_fp8b(h, _dims(h), codes, scales, offsets, Y, rows, R, stream)
+
+
+def _experts_linear_fp8b(h, dims, codes, scales, offsets, Y, rows, R, stream):
+    i32 = _torch().int32
+    M = codes.shape[0]
+    yrows, ycols, ldy = _matrix(Y, "Y")
+    R = yrows if R is None else R
+    ldc, lds = _fp8b_strides(codes, scales, M, dims.K if dims else codes.shape[1], 1)
+    if dims:
+        if yrows < R or ycols < dims.columns:
+            _too_small("Y", R, dims.columns)
+        _need_flat(offsets, i32, dims.experts + 1, "offsets")
+    if rows is not None:
+        _need_flat(rows, i32, R, "rows")
+    st = _lib().spense_experts_linear_fp8b(h, codes.data_ptr(), ldc, scales.data_ptr(), lds, M,
+                                           None if rows is None else rows.data_ptr(), offsets.data_ptr(), R,
+                                           Y.data_ptr(), dtype_of(Y), ldy, _stream(stream))
+    _check(st, "spense_experts_linear_fp8b")
+
+
+def _norm_matrix(t, rows: int, H: int, what: str):
+    r, c, ld = _matrix(t, what)
+    if r < rows or c < H:
+        _too_small(what, rows, H)
+    return t.data_ptr(), ld
+
+
+def spense_block_norm(O, residual, residual_out, Y, *, pre=None, post=None, gate=None, eps: float, scale: float = 1.0,
+                      yscales=None, pos=None, weights=None, stream=None) -> None:
+    """The pass over the rows between two blocks: o = O, or sum_j weights[t, j] O[pos[t, j]];
+    r = scale * residual + gate * (post: rms(o) * post, else o) into residual_out, rms(r) * pre into Y.
+
+    residual, residual_out and Y may be None (zeros; not stored), residual_out may be residual.  gate is [T, H], or [1, H] or
+    [H] for all rows.  With yscales (float32 [T, ceil(H / 128)]) Y holds bytes and receives fp8b codes."""
+    torch = _torch()
+    orows, H, ldo = _matrix(O, "O")
+    T = orows
+    kk = 0
+    if pos is not None:
+        T, kk = pos.shape
+        _need_flat(pos, torch.int32, 0, "pos")
+        if weights is None:
+            raise ValueError("pos needs weights")
+        _need_flat(weights, torch.float32, T * kk, "weights")
+    elif weights is not None:
+        raise ValueError("weights need pos")
+    wtype = gtype = rtype = ytype = 0
+    post_p = pre_p = gate_p = res_p = out_p = y_p = ys_p = None
+    ldg = ldr = ldro = ldy = lds = 0
+    for w in (post, pre):
+        if w is not None:
+            _need_flat(w, w.dtype, H, "post and pre")
+            wtype = dtype_of(w)
+    if post is not None and pre is not None and post.dtype is not pre.dtype:
+        raise TypeError(f"post is {post.dtype}, pre {pre.dtype}")
+    post_p, pre_p = _ptr(post), _ptr(pre)
+    if gate is not None:
+        gtype = dtype_of(gate)
+        if gate.dim() == 1 or gate.shape[0] == 1:
+            _need_flat(gate, gate.dtype, H, "gate")
+            gate_p = gate.data_ptr()
+        else:
+            gate_p, ldg = _norm_matrix(gate, T, H, "gate")
+    if residual is not None:
+        rtype = dtype_of(residual)
+        res_p, ldr = _norm_matrix(residual, T, H, "residual")
+    if residual_out is not None:
+        if residual is not None and residual_out.dtype is not residual.dtype:
+            raise TypeError(f"residual is {residual.dtype}, residual_out {residual_out.dtype}")
+        rtype = dtype_of(residual_out)
+        out_p, ldro = _norm_matrix(residual_out, T, H, "residual_out")
+    if Y is not None:
+        if yscales is not None:
+            ldy, lds = _fp8b_strides(Y, yscales, T, H, 1)
+            y_p, ys_p, ytype = Y.data_ptr(), yscales.data_ptr(), DT_FP8
+        else:
+            ytype = dtype_of(Y)
+            y_p, ldy = _norm_matrix(Y, T, H, "Y")
+    call = NormCall(T, H, O.data_ptr(), ldo, orows, _ptr(pos), _ptr(weights), post_p, pre_p, gate_p, ldg, res_p, ldr,
+                    out_p, ldro, y_p, ldy, ys_p, lds, kk, dtype_of(O), wtype, gtype, rtype, ytype, scale, eps)
+    _check(_lib().spense_block_norm(ctypes.byref(call), _stream(stream)), "spense_block_norm")
+
+
 def spense_info(h: int) -> dict:
     info = LayerInfo()
     _check(_lib().spense_info(h, ctypes.byref(info)), "spense_info")
@@ -655,4 +863,53 @@ class SpenseExperts(_Owned):
 
     def __call__(self, X, offsets, Y, *, rows=None, adtype: int = DT_BF16, stream=None):
         _experts_linear(self.handle, self._dims, X, offsets, Y, rows, adtype, None, stream)
+        return Y
+
+
+class SpenseLinearFp8b(_Owned):
+    """Owns one packed fp8b layer; ``layer(X, Y)`` runs spense_linear, ``layer.w8a8(X, Y)`` spense_linear_w8a8,
+    ``layer.quantized(codes, scales, Y)`` spense_linear_fp8b."""
+
+    def __init__(self, codes, scales, **kw):
+        self.handle = spense_pack_fp8b(codes, scales, **kw)
+        self.info = spense_info(self.handle)
+        self._dims = _dims(self.handle)
+
+    def _sizes(self, X, Y):
+        M, xcols, ldx = _matrix(X, "X")
+        yrows, ycols, ldy = _matrix(Y, "Y")
+        if xcols < self._dims.K:
+            _too_small("X", M, self._dims.K)
+        if yrows < M or ycols < self._dims.columns:
+            _too_small("Y", M, self._dims.columns)
+        return dict(M=M, ldx=ldx, ldy=ldy)
+
+    def __call__(self, X, Y, stream=None):
+        spense_linear(self.handle, X, Y, stream=stream, **self._sizes(X, Y))
+        return Y
+
+    def w8a8(self, X, Y, stream=None):
+        spense_linear_w8a8(self.handle, X, Y, stream=stream, **self._sizes(X, Y))
+        return Y
+
+    def quantized(self, codes, scales, Y, stream=None):
+        _linear_fp8b(self.handle, self._dims, codes, scales, Y, None, stream)
+        return Y
+
+
+class SpenseExpertsFp8b(_Owned):
+    """Owns the packed fp8b layers of a set of experts; ``experts(X, offsets, Y, rows=...)`` runs
+    spense_experts_linear, ``experts.quantized(codes, scales, offsets, Y, rows=...)`` spense_experts_linear_fp8b."""
+
+    def __init__(self, W, scales, **kw):
+        self.handle = spense_pack_experts_fp8b(W, scales, **kw)
+        self.info = spense_info(self.handle)
+        self._dims = _dims(self.handle)
+
+    def __call__(self, X, offsets, Y, *, rows=None, adtype: int = DT_BF16, stream=None):
+        _experts_linear(self.handle, self._dims, X, offsets, Y, rows, adtype, None, stream)
+        return Y
+
+    def quantized(self, codes, scales, offsets, Y, *, rows=None, stream=None):
+        _experts_linear_fp8b(self.handle, self._dims, codes, scales, offsets, Y, rows, None, stream)
         return Y

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libspense.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("spense_kernels.hip", "spense_tile.hip", "spense_score.hip",
                                                    "spense_experts.hip", "spense_mx.hip", "spense_route.hip",
-                                                   "spense_mx_api.cpp", "spense_api.cpp")]
+                                                   "spense_fp8b.hip", "spense_fp8b_linear.hip", "spense_norm.hip",
+                                                   "spense_mx_api.cpp", "spense_fp8b_api.cpp", "spense_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # -packed-fp32-ops: keep the compiler from forming v_pk_{add,mul,fma}_f32.
@@ -26,7 +27,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-
 # blocked accumulator tiles (up to 64 16x16 tiles per wave); above the default
 # size limit of a forced unroll the tile array would live in scratch memory.
 EXTRA = {f: ["-mllvm", "-pragma-unroll-threshold=200000"]
-         for f in ("spense_kernels.hip", "spense_tile.hip", "spense_experts.hip")}
+         for f in ("spense_kernels.hip", "spense_tile.hip", "spense_experts.hip", "spense_fp8b_linear.hip")}
 
 
 def _run(cmd):

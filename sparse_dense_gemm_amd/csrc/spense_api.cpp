@@ -15,46 +15,9 @@
 #include <vector>
 
 #include "../../include/spense.h"
-#include "spense_internal.h"
-#include "spense_mx.h"
-#include "spense_workspace.h"
+#include "spense_layer.h"
 
 using namespace spense;
-
-struct spense_layer {
-  LayerDesc d{};
-  int device = 0;
-  std::vector<int32_t> pi_host;
-  uint8_t* wpack = nullptr;
-  float* scales = nullptr;
-  int32_t* pi = nullptr;
-  int32_t* pip = nullptr;
-  float* vals32 = nullptr;
-  uint32_t* meta32 = nullptr;
-  float* dense32 = nullptr;
-  float* ws = nullptr;
-  size_t ws_bytes = 0;
-  void* xws = nullptr;  // activations in X'p order: gathered bf16 [M][K_p] (chunked staging of a chosen
-                        // dense set), or W8A8 e4m3 codes [M][K_p] followed by the token scales [M]
-  size_t xws_bytes = 0;
-  int32_t* counters = nullptr;
-  size_t n_counters = 0;
-  GraphKept<kWorkspaces> graphs;  // workspaces that captured calls hold
-  int32_t* ycol = nullptr;  // output column of each packed row, -1 on padding rows
-  int32_t* wrow = nullptr;  // W row of each packed row (parts of an output-split layer)
-  int64_t weight_bytes = 0;
-  int64_t device_bytes = 0;
-  // output-split layer (Technical Summary 2.A): no packed form of its own;
-  // part[0] holds the 2:4 rows (no dense columns), part[1] the dense rows (no
-  // sparse columns); either may be absent.  rho_host = [sparse rows | dense rows].
-  // 0 input-split layer, 1 output-split layer, 2 GLU block, 3 mx4 layer, 4 experts' layers
-  int split = 0;
-  ExpertsLayer* experts = nullptr;  // mx4 layer, experts' layers: their packed form
-  spense_layer* part[2] = {nullptr, nullptr};
-  spense_layer* down = nullptr;  // GLU block: the down projection (input-split, read in rho order)
-  int64_t N_s = 0, N_d = 0;
-  std::vector<int32_t> rho_host;
-};
 
 namespace {
 
@@ -76,6 +39,7 @@ void release(spense_layer* h) {
   release(h->part[1]);
   release(h->down);
   experts_release(h->experts);
+  delete h->grouped;
   void* ptrs[] = {h->wpack, h->scales, h->pi,      h->pip, h->vals32, h->meta32,
                   h->dense32, h->ws,   h->counters, h->xws, h->ycol,   h->wrow};
   for (void* p : ptrs)
@@ -1022,14 +986,15 @@ static int new_experts(const void* W, int32_t wdtype, const uint8_t* scales, int
   return rc;
 }
 
-// The mx4 layer with activations left in bf16 or quantised (adtype).
-static int mx4_linear_call(spense_handle h, const void* X, int32_t xdtype, int32_t adtype, int64_t M, int64_t ldx,
+// The mx4 or fp8b layer with activations left in bf16 or quantised (adtype).
+static int one_expert_call(spense_handle h, const void* X, int32_t xdtype, int32_t adtype, int64_t M, int64_t ldx,
                            void* Y, int32_t ydtype, int64_t ldy, void* stream) {
-  const ExpertsDesc& d = experts_desc(h->experts);
+  const ExpertsDesc& d = h->grouped ? h->grouped->desc() : experts_desc(h->experts);
   if (M < 1 || M > (int64_t(1) << 24) || ldx < d.K || ldy < d.N) return SPENSE_EINVAL;
   if (ldx >= kMaxLd) return SPENSE_EUNSUPPORTED;
   if (!valid_dtype(xdtype) || !valid_dtype(ydtype)) return SPENSE_EINVAL;
   if (xdtype != SPENSE_BF16 || ydtype == SPENSE_FP8_E4M3) return SPENSE_EUNSUPPORTED;
+  if (h->grouped) return h->grouped->run(X, adtype, M, ldx, nullptr, nullptr, M, Y, ydtype, ldy, (hipStream_t)stream);
   return experts_run(h->experts, X, adtype, M, ldx, nullptr, nullptr, M, Y, ydtype, ldy, (hipStream_t)stream);
 }
 
@@ -1038,10 +1003,10 @@ static int mx4_linear_call(spense_handle h, const void* X, int32_t xdtype, int32
 static int linear_call(spense_handle h, const void* X, int32_t xdtype, int64_t M, int64_t ldx, void* Y,
                        int32_t ydtype, int64_t ldy, int32_t splits, void* stream, bool noalloc) {
   if (!h || !X || !Y) return SPENSE_EINVAL;
-  if (h->split == 2 || h->split == 4) return SPENSE_EINVAL;  // spense_glu, spense_experts_linear
-  if (h->split == 3) {  // no split-K factor to force, no form that allocates nothing
+  if (h->split == 2 || h->split == 4 || h->split == 6) return SPENSE_EINVAL;  // spense_glu, spense_experts_linear
+  if (h->split == 3 || h->split == 5) {  // no split-K factor to force, no form that allocates nothing
     if (noalloc || splits != 0) return SPENSE_EUNSUPPORTED;
-    return mx4_linear_call(h, X, xdtype, SPENSE_BF16, M, ldx, Y, ydtype, ldy, stream);
+    return one_expert_call(h, X, xdtype, SPENSE_BF16, M, ldx, Y, ydtype, ldy, stream);
   }
   const LayerDesc& d = h->d;
   if (M < 1 || M > (int64_t(1) << 24) || ldx < d.K || ldy < d.N) return SPENSE_EINVAL;
@@ -1099,6 +1064,9 @@ int spense_quantize_tokens(const void* X, int64_t M, int64_t K, int64_t ldx, uin
 int spense_linear_w8a8(spense_handle h, const void* X, int64_t M, int64_t ldx, void* Y, int32_t ydtype, int64_t ldy,
                        int32_t splits, void* stream) {
   if (!h || !X || !Y) return SPENSE_EINVAL;
+  if (h->split == 5)  // no split-K factor to force
+    return splits ? SPENSE_EUNSUPPORTED
+                  : one_expert_call(h, X, SPENSE_BF16, SPENSE_FP8_E4M3, M, ldx, Y, ydtype, ldy, stream);
   if (h->split != 0) return SPENSE_EUNSUPPORTED;  // input-split layers only
   const LayerDesc& d = h->d;
   if (d.wdtype != SPENSE_FP8_E4M3) return SPENSE_EUNSUPPORTED;
@@ -1252,6 +1220,10 @@ int spense_info(spense_handle h, spense_layer_info* info) {
     experts_info(h->experts, info);
     return SPENSE_OK;
   }
+  if (h->grouped) {
+    h->grouped->info(info);
+    return SPENSE_OK;
+  }
   info->N = h->d.N;
   info->K = h->d.K;
   info->K_s = h->d.K_s;
@@ -1331,7 +1303,7 @@ int spense_linear_w4a4(spense_handle h, const void* X, int64_t M, int64_t ldx, v
                        void* stream) {
   if (!h || !X || !Y) return SPENSE_EINVAL;
   if (h->split != 3) return SPENSE_EUNSUPPORTED;
-  return mx4_linear_call(h, X, SPENSE_BF16, SPENSE_MX4, M, ldx, Y, ydtype, ldy, stream);
+  return one_expert_call(h, X, SPENSE_BF16, SPENSE_MX4, M, ldx, Y, ydtype, ldy, stream);
 }
 
 int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, int64_t E, int64_t N, int64_t K,
@@ -1352,17 +1324,18 @@ int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, in
 
 int spense_experts_linear(spense_handle h, const void* X, int32_t adtype, int64_t M, int64_t ldx, const int32_t* rows,
                           const int32_t* offsets, int64_t R, void* Y, int32_t ydtype, int64_t ldy, void* stream) {
-  if (!h || h->split != 4 || !offsets || (R > 0 && (!X || !Y))) return SPENSE_EINVAL;
-  const ExpertsDesc& d = experts_desc(h->experts);
+  if (!h || (h->split != 4 && h->split != 6) || !offsets || (R > 0 && (!X || !Y))) return SPENSE_EINVAL;
+  const ExpertsDesc& d = h->grouped ? h->grouped->desc() : experts_desc(h->experts);
   if (M < (R ? 1 : 0) || M > (int64_t(1) << 24) || R < 0 || R > (int64_t(1) << 24)) return SPENSE_EINVAL;
   if (!rows && M < R) return SPENSE_EINVAL;
   if (ldx < d.K || ldy < (d.glu ? d.N / 2 : d.N)) return SPENSE_EINVAL;
-  if (adtype != SPENSE_BF16 && adtype != SPENSE_MX4)
-    return valid_dtype(adtype) ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
+  if (adtype != SPENSE_BF16 && adtype != (h->grouped ? SPENSE_FP8_E4M3 : SPENSE_MX4))
+    return valid_dtype(adtype) || adtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
   if (ydtype != SPENSE_F32 && ydtype != SPENSE_BF16)
     return ydtype == SPENSE_FP8_E4M3 || ydtype == SPENSE_MX4 ? SPENSE_EUNSUPPORTED : SPENSE_EINVAL;
   if (ldx >= kMaxLd || (adtype == SPENSE_MX4 && d.wdtype != SPENSE_MX4)) return SPENSE_EUNSUPPORTED;
   if (R == 0) return SPENSE_OK;
+  if (h->grouped) return h->grouped->run(X, adtype, M, ldx, rows, offsets, R, Y, ydtype, ldy, (hipStream_t)stream);
   return experts_run(h->experts, X, adtype, M, ldx, rows, offsets, R, Y, ydtype, ldy, (hipStream_t)stream);
 }
 

@@ -3,13 +3,9 @@
 // spense_api.cpp.
 #include <algorithm>
 #include <cmath>
-#include <cstdio>
-#include <cstdlib>
 #include <new>
 
-#include "../../include/spense.h"
-#include "spense_mx.h"
-#include "spense_workspace.h"
+#include "spense_product.h"
 
 namespace spense {
 
@@ -17,30 +13,13 @@ struct ExpertsLayer {
   ExpertsDesc d{};
   int64_t weight_bytes = 0;
   int64_t device_bytes = 0;
-  // workspaces, shared by the calls on the handle (one in flight)
-  uint8_t* xws = nullptr;  // activations laid out for the product kernel
-  size_t xws_bytes = 0;
-  float* ws = nullptr;     // partial sums
-  size_t ws_bytes = 0;
-  int32_t* counters = nullptr;
-  size_t n_counters = 0;
-  GraphKept<kWorkspaces> graphs;  // workspaces that captured calls hold
+  ProductWorkspaces w;
   // rows that ws and counters have been sized for, whatever split count a
   // smaller call's plan takes: [mx4 activations][grouped]
   int64_t sized[2][2] = {{0, 0}, {0, 0}};
 };
 
 namespace {
-
-constexpr int64_t kMaxPartials = int64_t(64) << 20;  // bytes of partial sums a plan may ask for
-constexpr int kCUs = 256;
-
-int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
-
-int status_of(hipError_t e) {
-  const int rc = report_hip(e);
-  return e == hipErrorOutOfMemory ? SPENSE_ENOMEM : rc;
-}
 
 // Estimated cycles of a launch of `groups` m-groups.  Per stage (256 bytes of
 // every activation row) a workgroup multiplies 4 waves r t operand pairs at 16
@@ -77,119 +56,18 @@ double plan_cycles(const ExpertsDesc& d, int config, int64_t S, double groups, i
   return t;
 }
 
-// Launch plan of R grouped rows (a function of ceil(R / 16) only, so that the
-// workspaces of every smaller call can be sized by stepping over it): of the
-// kernel's configurations and the split counts that fill one or two workgroups
-// per CU, the one with the least estimated time.
 ExpertsPlan make_plan(const ExpertsDesc& d, bool grouped, int64_t R, bool xmx) {
-  // forced by SPENSE_EXPERTS=config[,splits[,rblock[,run]]] (tests, tuning)
-  int f_config = -1, f_splits = 0, f_rblock = 0, f_run = 0;
-  if (const char* v = getenv("SPENSE_EXPERTS")) {
-    sscanf(v, "%d,%d,%d,%d", &f_config, &f_splits, &f_rblock, &f_run);
-    if (f_config >= experts_config_count()) f_config = -1;
-  }
-  const int64_t R16 = (R + 15) / 16 * 16;
-  const int64_t hit = grouped ? std::min(d.E, R16) : 1;  // experts that may have rows
-  const int64_t rows = (R16 + hit - 1) / hit;            // rows of one, on average
-  const int64_t stages = xmx ? (d.NU + 3) / 4 : d.NU;
-  ExpertsPlan p{};
-  double best = 0.0;
-  for (int i = 0; i < experts_config_count(); ++i) {
-    if (f_config >= 0 && i != f_config) continue;
-    const ExpertsShape c = experts_shape(i);
-    const int64_t per = c.waves * c.r, take = 16 * c.t;
-    const int64_t rg = (d.NT + per - 1) / per;
-    // sum over experts of ceil(n / take) for any split of R rows over `hit` experts
-    const int64_t mg = grouped ? (R16 - hit) / take + hit : (R16 + take - 1) / take;
-    // of them with rows: groups of no particular size leave half of their last m-group empty
-    const double busy =
-        grouped && hit > 1 ? (double)hit * std::max(1.0, (double)rows / (double)take + 0.5) : (double)mg;
-    const int64_t most = std::min<int64_t>(std::max<int64_t>(1, stages / (xmx ? 2 : 4)), 64);
-    int64_t tried = 0;
-    for (int k = 0; k <= 2; ++k) {
-      int64_t S = k == 0 ? 1 : std::min<int64_t>(most, (int64_t)(k * kCUs / ((double)rg * busy)));
-      if (f_splits > 0) S = std::min<int64_t>(f_splits, std::min<int64_t>(stages, 64));
-      while (S > 1 && S * d.NT * R16 * 64 > kMaxPartials) --S;
-      if (S <= tried) continue;
-      tried = S;
-      const double t = plan_cycles(d, i, S, busy, hit, R16, xmx);
-      if (best == 0.0 || t < best) {
-        best = t;
-        p.config = i;
-        p.splits = (int)S;
-        p.rgroups = (int)rg;
-        p.mgroups = (int)mg;
-      }
-    }
-  }
-  const ExpertsShape c = experts_shape(p.config);
-  // Launch order: large groups in blocks of four row groups, m-group by m-group
-  // (the two workgroups of a CU, 32 apart, then share their row group's
-  // weights), small ones, whose weights are most of what is read, m-group by
-  // m-group of a single row group.
-  p.rblock = f_rblock > 0 ? f_rblock : c.t >= 8 ? std::min(p.rgroups, 4) : 1;
-  p.run = f_run;
-  return p;
-}
-
-struct Need {
-  int64_t xws = 0, ws = 0, cnt = 0;
-  void grow(const Need& o) {
-    xws = std::max(xws, o.xws);
-    ws = std::max(ws, o.ws);
-    cnt = std::max(cnt, o.cnt);
-  }
-};
-
-Need plan_need(const ExpertsDesc& d, const ExpertsPlan& p, int64_t R) {
-  Need n;
-  if (p.splits > 1) {
-    n.ws = (int64_t)p.splits * d.NT * ((R + 15) / 16 * 16) * 64;
-    n.cnt = (int64_t)p.rgroups * p.mgroups;
-  }
-  return n;
-}
-
-bool fits(const ExpertsLayer* h, const Need& n) {
-  return (int64_t)h->xws_bytes >= n.xws && (int64_t)h->ws_bytes >= n.ws && (int64_t)h->n_counters >= n.cnt;
-}
-
-// Replaces the workspaces that are too small (earlier launches may still use
-// them, so the stream is synchronised first; those that a graph may hold stay).
-int grow(ExpertsLayer* h, const Need& n, hipStream_t s) {
-  hipError_t e = hipStreamSynchronize(s);
-  if (e != hipSuccess) return status_of(e);
-  auto regrow = [&](int which, void** p, size_t& have, int64_t want) -> int {
-    if (want <= (int64_t)have) return SPENSE_OK;
-    if (!h->graphs.drop(which, *p)) return SPENSE_ENOMEM;
-    *p = nullptr;
-    have = 0;
-    const hipError_t err = hipMalloc(p, (size_t)want);
-    if (err != hipSuccess) return status_of(err);
-    have = (size_t)want;
-    return SPENSE_OK;
-  };
-  int rc = regrow(kWsX, (void**)&h->xws, h->xws_bytes, n.xws);
-  if (rc == SPENSE_OK) rc = regrow(kWsPartials, (void**)&h->ws, h->ws_bytes, n.ws);
-  if (rc == SPENSE_OK && n.cnt > (int64_t)h->n_counters) {
-    size_t bytes = h->n_counters * 4;
-    rc = regrow(kWsCounters, (void**)&h->counters, bytes, n.cnt * 4);
-    h->n_counters = bytes / 4;
-    if (rc == SPENSE_OK) {
-      e = launch_zero_i32(h->counters, n.cnt, s);
-      if (e != hipSuccess) rc = status_of(e);
-    }
-  }
-  return rc;
+  return choose_plan(
+      d, grouped, R, xmx ? (d.NU + 3) / 4 : d.NU, xmx ? 2 : 4, experts_config_count(), experts_shape,
+      [&](int i, int64_t S, double groups, int64_t hit, int64_t R16) { return plan_cycles(d, i, S, groups, hit, R16, xmx); },
+      "SPENSE_EXPERTS");
 }
 
 }  // namespace
 
 void experts_release(ExpertsLayer* h) {
   if (!h) return;
-  void* ptrs[] = {h->d.wpack, h->xws, h->ws, h->counters};
-  for (void* p : ptrs)
-    if (p) (void)hipFree(p);
+  if (h->d.wpack) (void)hipFree(h->d.wpack);
   delete h;
 }
 
@@ -254,7 +132,6 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
   // gathered if they are picked by index, or X's own if it has no more than R and
   // lies within 31 bits.  So a call with fewer rows of X or in Y never needs a
   // larger workspace.
-  constexpr int64_t kSpan = int64_t(1) << 31;
   Need need = plan_need(d, p, R);
   bool prepare = true;
   if (xmx) {
@@ -275,31 +152,31 @@ int experts_run(ExpertsLayer* h, const void* X, int32_t adtype, int64_t M, int64
   if (R > sized) {  // every smaller call too: none of them may allocate later (graph capture)
     for (int64_t r = (sized / 16 + 1) * 16; r < R; r += 16) need.grow(plan_need(d, make_plan(d, offsets != nullptr, r, xmx), r));
   }
-  if (!fits(h, need)) {
-    const int rc = grow(h, need, s);
+  if (!h->w.fits(need)) {
+    const int rc = h->w.grow(need, s);
     if (rc != SPENSE_OK) return rc;
   }
   sized = std::max(sized, R);
-  if (need.xws || need.ws) h->graphs.used(s);
+  if (need.xws || need.ws) h->w.graphs.used(s);
   hipError_t e = hipSuccess;
   a.M = M;
   if (prepare) {
     const int32_t* pick = gather ? rows : nullptr;
     if (xmx) {
-      a.xs = h->xws + codes_bytes;
-      e = launch_mx4_activations(X, M, d.K, ldx, pick, n_rows, h->xws, a.ldx, h->xws + codes_bytes, a.ldxs, s);
+      a.xs = h->w.xws + codes_bytes;
+      e = launch_mx4_activations(X, M, d.K, ldx, pick, n_rows, h->w.xws, a.ldx, h->w.xws + codes_bytes, a.ldxs, s);
     } else {
-      e = launch_pad_rows(X, M, d.K, ldx, pick, n_rows, h->xws, a.ldx, s);
+      e = launch_pad_rows(X, M, d.K, ldx, pick, n_rows, h->w.xws, a.ldx, s);
     }
     if (e != hipSuccess) return status_of(e);
-    a.X = h->xws;
+    a.X = h->w.xws;
     a.M = n_rows;
     if (gather) a.rows = nullptr;
   } else {
     a.X = (const uint8_t*)X;
   }
-  a.ws = h->ws;
-  a.counters = h->counters;
+  a.ws = h->w.ws;
+  a.counters = h->w.counters;
   e = launch_experts(d, a, xmx ? DT_MX4 : DT_BF16, p, s);
   return e == hipSuccess ? SPENSE_OK : status_of(e);
 }
