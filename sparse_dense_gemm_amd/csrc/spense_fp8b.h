@@ -7,7 +7,7 @@
 // Packed weights.  An expert's N rows are padded to row tiles of 16 (the rows
 // of a matrix instruction), K to units of 128 columns.  Per row tile
 //   [units][2 halves][64 lanes][16 B], lane l holding row l % 16, columns
-//   32 (l / 16) + 16 half .. + 15 of the unit,
+//   64 half + 16 (l / 16) .. + 15 of the unit,
 // so a lane's two pieces are its operand of a 16x16x128 product as they are
 // (e4m3 activations), and eight codes at a time, widened, its operands of four
 // 16x16x32 products (bf16 activations); a wave streams whole kilobytes.
@@ -31,13 +31,16 @@ struct Fp8bDesc : ExpertsDesc {  // wdtype DT_FP8, tile_bytes = NU * 2048
   float* scales;                 // E * SG * NUe * 2
 };
 
+// Products: bf16 rows; codes on the instruction for codes (Y in bf16); codes widened to bf16 (Y in fp32).
+enum Fp8bKind : int32_t { kBf16 = 0, kCodes = 1, kWide = 2 };
+
 struct Fp8bArgs : ExpertsArgs {  // X: bf16 rows, or codes with scales at xs (row stride ldxs bytes)
-  int32_t codes;                 // 1: X holds codes
+  Fp8bKind kind;
 };
 
-// The configurations of spense_fp8b_linear.hip (codes: those for e4m3 activations).
-int fp8b_config_count(bool codes);
-ExpertsShape fp8b_shape(bool codes, int config);
+// The configurations of spense_fp8b_linear.hip.
+int fp8b_config_count(Fp8bKind kind);
+ExpertsShape fp8b_shape(Fp8bKind kind, int config);
 hipError_t launch_fp8b_linear(const Fp8bDesc& d, const Fp8bArgs& a, const ExpertsPlan& p, hipStream_t s);
 
 // ---- spense_fp8b.hip ----

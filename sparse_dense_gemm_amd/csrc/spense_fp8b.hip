@@ -154,7 +154,7 @@ __global__ __launch_bounds__(256) void pack_kernel(Fp8bDesc d, int64_t t0, int64
   const int64_t tile = t0 + i;
   const int64_t e = tile / d.NT, rt = tile - e * d.NT;
   const int64_t src = packed_row(d, rt * 16 + (lane & 15));
-  const int64_t k = (int64_t)(u >> 1) * kUnitK + 32 * (lane >> 4) + 16 * (u & 1);
+  const int64_t k = (int64_t)(u >> 1) * kUnitK + 64 * (u & 1) + 16 * (lane >> 4);
   u32x4 o = u32x4{0, 0, 0, 0};
   if (src >= 0) {
     const uint8_t* w = W + (e * d.N + src) * ldw + k;

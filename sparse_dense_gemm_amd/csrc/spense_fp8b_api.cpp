@@ -34,10 +34,11 @@ bool matrix_ok(int64_t M, int64_t K, int64_t ldc, int64_t lds) {
 // its weights take from memory.  Two workgroups run together on a CU.  With
 // split K every sum is written and read once more, and a workgroup reads its
 // tile's S sums by itself.
-double plan_cycles(const Fp8bDesc& d, bool codes, int config, int64_t S, double groups, int64_t hit, int64_t R) {
-  const ExpertsShape c = fp8b_shape(codes, config);
+double plan_cycles(const Fp8bDesc& d, Fp8bKind kind, int config, int64_t S, double groups, int64_t hit, int64_t R) {
+  const ExpertsShape c = fp8b_shape(kind, config);
+  const bool codes = kind != kBf16;
   const double wkb = (codes ? 4.0 : 2.0) * c.waves * c.r, xkb = 4.0 * c.t;
-  const double work = (16.0 * c.waves * c.r * c.t + 16.0 * (wkb + xkb)) * (c.t < 4 ? 1.3 : c.t == 4 ? 1.45 : 1.0) + 60.0;
+  const double work = ((kind == kWide ? 32.0 : 16.0) * c.waves * c.r * c.t + 16.0 * (wkb + xkb)) * (c.t < 4 ? 1.3 : c.t == 4 ? 1.45 : 1.0) + 60.0;
   const double latency = c.stages > 1 ? 3000.0 / c.stages : 2000.0;
   const int64_t rg = (d.NT + c.waves * c.r - 1) / (c.waves * c.r);
   const int64_t stages = ((codes ? (d.NU + 1) / 2 : d.NU) + S - 1) / S;
@@ -57,11 +58,12 @@ double plan_cycles(const Fp8bDesc& d, bool codes, int config, int64_t S, double 
   return t;
 }
 
-ExpertsPlan make_plan(const Fp8bDesc& d, bool grouped, int64_t R, bool codes) {
+ExpertsPlan make_plan(const Fp8bDesc& d, bool grouped, int64_t R, Fp8bKind kind) {
+  const bool codes = kind != kBf16;
   return choose_plan(
-      d, grouped, R, codes ? (d.NU + 1) / 2 : d.NU, codes ? 2 : 4, fp8b_config_count(codes),
-      [&](int i) { return fp8b_shape(codes, i); },
-      [&](int i, int64_t S, double groups, int64_t hit, int64_t R16) { return plan_cycles(d, codes, i, S, groups, hit, R16); },
+      d, grouped, R, codes ? (d.NU + 1) / 2 : d.NU, codes ? 2 : 4, fp8b_config_count(kind),
+      [&](int i) { return fp8b_shape(kind, i); },
+      [&](int i, int64_t S, double groups, int64_t hit, int64_t R16) { return plan_cycles(d, kind, i, S, groups, hit, R16); },
       "SPENSE_FP8B");
 }
 
@@ -79,8 +81,8 @@ struct Fp8bLayer final : GroupedLayer {
   int64_t weight_bytes = 0, device_bytes = 0;
   ProductWorkspaces w;
   // rows that the partial sums and counters have been sized for, whatever split
-  // count a smaller call's plan takes: [codes][grouped]
-  int64_t sized[2][2] = {{0, 0}, {0, 0}};
+  // count a smaller call's plan takes: [kind][grouped]
+  int64_t sized[3][2] = {{0, 0}, {0, 0}, {0, 0}};
 
   ~Fp8bLayer() override {
     if (d.wpack) (void)hipFree(d.wpack);
@@ -108,7 +110,8 @@ struct Fp8bLayer final : GroupedLayer {
   int call(const Activations& x, int64_t M, const int32_t* rows, const int32_t* offsets, int64_t R, void* Y,
            int32_t ydtype, int64_t ldy, hipStream_t s) {
     const bool grouped = offsets != nullptr, codes = x.quantize || x.scales;
-    const ExpertsPlan p = make_plan(d, grouped, R, codes);
+    const Fp8bKind kind = !codes ? kBf16 : ydtype == SPENSE_F32 ? kWide : kCodes;
+    const ExpertsPlan p = make_plan(d, grouped, R, kind);
     Fp8bArgs a{};
     a.rows = rows;
     a.offsets = offsets;
@@ -116,7 +119,7 @@ struct Fp8bLayer final : GroupedLayer {
     a.Y = Y;
     a.ldy = ldy;
     a.ydtype = ydtype;
-    a.codes = codes;
+    a.kind = kind;
     // The product kernel reads rows of 16-byte pieces through offsets of 31
     // bits: activations are quantised into that form, or read in place if they
     // have it and laid out first if not: the R rows that are read, gathered if
@@ -143,9 +146,9 @@ struct Fp8bLayer final : GroupedLayer {
     const int64_t n_rows = rows && !gather ? M : R;
     const int64_t codes_bytes = codes ? align256(n_rows * a.ldx) : 0;
     if (prepare) need.xws = codes ? codes_bytes + n_rows * a.ldxs : n_rows * a.ldx;
-    int64_t& have = sized[codes][grouped];
+    int64_t& have = sized[kind][grouped];
     if (R > have) {  // every smaller call too: none of them may allocate later (graph capture)
-      for (int64_t r = (have / 16 + 1) * 16; r < R; r += 16) need.grow(plan_need(d, make_plan(d, grouped, r, codes), r));
+      for (int64_t r = (have / 16 + 1) * 16; r < R; r += 16) need.grow(plan_need(d, make_plan(d, grouped, r, kind), r));
     }
     if (!w.fits(need)) {
       const int rc = w.grow(need, s);

@@ -4,13 +4,23 @@
 //
 //   Y[r, n] = sum_b sx[r, b] sw[n, b] sum_(k in b) x[r, k] w_e[n, k],   o_e <= r < o_(e+1),
 //
-// over blocks b of 128 columns: with codes x the inner sum is one 16x16x128
-// product, with bf16 x (sx = 1) four 16x16x32 products on the weights widened
-// exactly in registers.  It starts from zero and is added to the sums by a fused
-// multiply-add with the product of the two scales, in 32 bits: a scale that is no
-// power of two cannot go through the matrix instruction's own scale operand, and
-// rounding it into an operand would lose bits.  That is four vector instructions
-// to each 16x16x128, which takes the time of eight, so they run beside it.
+// over blocks b of 128 columns.  The inner sum starts from zero and is added to
+// the sums by a fused multiply-add with the product of the two scales, in 32
+// bits: a scale that is no power of two cannot go through the matrix
+// instruction's own scale operand, and rounding it into an operand would lose
+// bits.  Three kinds of inner sums:
+//   kBf16   bf16 x (sx = 1): four 16x16x32 products on the weights widened exactly
+//           in registers;
+//   kCodes  codes x, Y in bf16: one 16x16x128 product of codes.  The instruction
+//           sums eight consecutive products at a time and drops what lies more than
+//           13 bits below the largest of them (a product of 2^2 beside one of 2^16;
+//           measured, and the same of 16x16x32 and with any operand as the eight);
+//           on normal inputs that is 2e-5 of the result, a hundredth of the rounding
+//           to bf16, for 3.5 times the rate of the 16x16x32 products;
+//   kWide   codes x, Y in fp32: both widened to bf16, whose products and sums keep
+//           the bits (6e-8 of the result).
+// The scales cost four vector instructions to each 16x16x128, which takes the time
+// of eight, so they run beside it.
 //
 // Tiles, launch order, split K and the way into Y are those of the products in
 // spense_experts.hip: a workgroup owns NW R row tiles (16 R NW output columns)
@@ -37,6 +47,12 @@ namespace {
   X(1, 4, 1, 2, 4, 2)               \
   X(2, 8, 1, 4, 2, 2)               \
   X(3, 4, 2, 8, 1, 2)               \
+  X(4, 4, 4, 8, 1, 2)
+#define SPENSE_FP8B_WIDE_CONFIGS(X) \
+  X(0, 8, 1, 1, 8, 2)               \
+  X(1, 4, 1, 2, 4, 2)               \
+  X(2, 8, 1, 4, 2, 2)               \
+  X(3, 4, 2, 8, 1, 2)               \
   X(4, 4, 4, 4, 1, 2)
 
 __device__ __forceinline__ f32x4 mfma_bf16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
@@ -51,9 +67,9 @@ __device__ __forceinline__ f32x4 mfma_e4m3(const u32x4& a0, const u32x4& a1, con
                                                           f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// XQ: activations are codes (true) or bf16 (false)
-template <bool XQ, int NW, int R, int T, int D, int WPS>
+template <int KIND, int NW, int R, int T, int D, int WPS>
 __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs a, ExpertsPlan p) {
+  constexpr bool XQ = KIND != kBf16;                     // activations are codes
   constexpr int kRows = 16 * T;
   constexpr int NU = XQ ? 2 : 1;                         // units of a stage
   constexpr uint32_t kStage = kRows * kStageBytes;       // a stage's rows in LDS
@@ -101,11 +117,14 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
   const uint32_t tb = (uint32_t)d.tile_bytes;
   u32x4 w[D][R][NL];
   float sw[kSpread ? 2 : D][2 * NU];  // [unit][even, odd packed rows]
+  // Piece i of row tile r for stage c: the stage's place is one scalar, chosen once
+  // (beyond the resource past the last stage, and past the last unit for the
+  // second unit's pieces), the row tile's a sum, the piece's a constant of the load.
   auto load_w = [&](auto slot, int r, int i, int c) __attribute__((always_inline)) {
     const int st = lo + c;
-    const bool in = c < n && (!XQ || 2 * st + i / 2 < (int)d.NU);
-    w[decltype(slot)::value][r][i] =
-        buf_load16(wr, 16 * lane, in ? (uint32_t)r * tb + (uint32_t)(NL * st + i) * 1024u : kOutOfRange);
+    const bool in = c < n && (!XQ || i < 2 || 2 * st + 1 < (int)d.NU);
+    const uint32_t at = in ? (uint32_t)st * (NL * 1024u) : kOutOfRange;
+    w[decltype(slot)::value][r][i] = buf_load16(wr, 16 * lane + 1024 * i, at + (uint32_t)r * tb);
   };
   auto load_scales = [&](auto slot, int c) __attribute__((always_inline)) {
     const uint32_t off = c < n ? (uint32_t)(lo + c) * (8u * NU) : kOutOfRange;
@@ -121,18 +140,19 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
     }
   };
 
-  // ---- activations.  A copy takes four rows x 256 bytes: lane l row l / 16,
-  // piece (l % 16) ^ ((row - 4) % 16) of 16 bytes.  A read of 16 bytes a lane
-  // serves 16 lanes at a time, rows 0-3 and 12-15 of one piece with rows 4-11 of
-  // the next lane group's: with that shift they hit different banks for both
-  // orders of the pieces, which differ between lane groups in the low three bits
-  // or agree in the high one.  Rows past the group and bytes past the row take an
-  // offset beyond the resource and land as zeros. ----
-  constexpr int kQ = 4 * T;                           // copies of a stage
-  constexpr int kPer = D * kQ / NW;                   // copies of a buffer per wave
-  constexpr int kRowsPer = kQ >= NW ? kQ / NW : 1;    // different rows among them
-  static_assert(NW % 4 == 0, "a wave's copies have the same rows modulo 16");
-  static_assert(D * kQ % NW == 0 && (kQ % NW == 0 || NW % kQ == 0), "every wave copies the same share");
+  // ---- activations.  In LDS a stage of an m-tile is four chunks of 64 bytes of
+  // its 16 rows, one copy each: lane l brings row l / 4 and, of the chunk's four
+  // pieces of 16 bytes, piece (l % 4) ^ f(row), f = 3 from row 8 on.  A read of 16
+  // bytes a lane serves 16 lanes at a time, rows 0-3 and 12-15 of one lane group
+  // with rows 4-11 of the next; with that shift they hit different banks where the
+  // two groups' pieces are neighbours (codes) and where they are two apart (bf16).
+  // A chunk needs no more than a lane's row to be addressed, so a wave that copies
+  // two m-tiles keeps two offsets (four rows x 256 bytes a copy: eight, and four
+  // for the reads, that the largest block does not have).  Rows past the group and
+  // bytes past the row take an offset beyond the resource and land as zeros. ----
+  constexpr int kPer = D * 4 * T / NW;                // copies of a buffer per wave
+  constexpr int kTiles = T >= NW ? T / NW : 1;        // different m-tiles among them
+  static_assert(T >= NW ? T % NW == 0 : NW % T == 0 && D % (NW / T) == 0, "every wave copies the same share");
   const int64_t xrow0 = a.rows ? 0 : row0;
   const int64_t xrows = a.rows ? a.M : cnt;
   const i32x4 xr = rsrc_words(a.X + xrow0 * a.ldx, (uint32_t)((xrows - 1) * a.ldx + a.xbytes));
@@ -142,13 +162,14 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
     const int64_t q = a.rows[row0 + local];
     return q < 0 || q >= a.M ? 0xFFFFFFFFu : (uint32_t)q;
   };
-  const int q0 = kQ >= NW ? wave : wave % kQ;
-  const int cr = lane >> 4, piece = (lane & 15) ^ ((4 * (q0 & 3) + cr - 4) & 15);
-  uint32_t xo[kRowsPer];
+  const int tile0 = T >= NW ? wave * kTiles : wave % T;
+  const int piece = 16 * ((lane & 3) ^ (lane & 32 ? 3 : 0));  // bytes into the chunk
+  const int limit = (int)a.xbytes - piece;  // of a chunk's place in the row
+  uint32_t xo[kTiles];
 #pragma unroll
-  for (int i = 0; i < kRowsPer; ++i) {
-    const uint32_t r = x_row(4 * (q0 + NW * i) + cr);
-    xo[i] = r == 0xFFFFFFFFu ? kOutOfRange : r * (uint32_t)a.ldx + 16u * piece;
+  for (int i = 0; i < kTiles; ++i) {
+    const uint32_t r = x_row(16 * (tile0 + i) + (lane >> 2));
+    xo[i] = r == 0xFFFFFFFFu ? kOutOfRange : r * (uint32_t)a.ldx + (uint32_t)piece;
   }
   // scales of codes: a copy takes 32 (row, unit) pairs twice over, lane l pair l of [stage][row][unit]
   constexpr int kSC = XQ ? D * kRows * 2 / 64 : 0;    // copies of a buffer (D T is even)
@@ -171,12 +192,13 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
   auto copy_one = [&](int c, uint32_t buf, auto ic) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value;
     if constexpr (i < kPer) {
-      const int q = kQ >= NW ? wave + NW * (i % kRowsPer) : q0;
-      const int st = kQ >= NW ? i / kRowsPer : wave / kQ + i * (NW / kQ);
+      constexpr int chunk = i % 4;
+      const int tile = T >= NW ? tile0 + i / 4 : tile0;
+      const int st = T >= NW ? 0 : wave / T + (NW / T) * (i / 4);
       const int at = lo + c + st;  // stage of K
-      const int left = (int)a.xbytes - at * kStageBytes;
-      const uint32_t v = 16 * piece >= left || at >= hi ? kOutOfRange : xo[i % kRowsPer];
-      copy16<false>(xr, buf + st * kStage + q * 1024u, v, (uint32_t)(at < hi ? at * kStageBytes : 0));
+      const int byte = at < hi ? at * kStageBytes + 64 * chunk : 0x7FFFFFFF;
+      const uint32_t v = byte >= limit ? kOutOfRange : xo[T >= NW ? i / 4 : 0];
+      copy16<false>(xr, buf + st * kStage + (4 * tile + chunk) * 1024u, v, (uint32_t)byte & 0x3FFFFFFFu);
     } else {
       const int id = wave + NW * (i - kPer);
       const int st = (64 * id + lane) / (2 * kRows), at = lo + c + st;  // one stage for all lanes, or several
@@ -190,14 +212,11 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
     static_for<0, kCopies>([&](auto ic) __attribute__((always_inline)) { copy_one(c, buf, ic); });
   };
 
-  // this lane's pieces of row lane % 16: codes, unit i / 2, half i % 2; bf16, step i
-  const int fr = lane & 15;
-  uint32_t fo[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pc = XQ ? 8 * (i >> 1) + 2 * g + (i & 1) : 4 * g + i;
-    fo[i] = (uint32_t)(fr * kStageBytes + 16 * (pc ^ ((fr - 4) & 15)));
-  }
+  // this lane's piece of row lane % 16: codes, chunk 2 unit + half, piece g of it;
+  // bf16, chunk 2 half + g / 2, pieces 2 (g % 2) and the next
+  const int fr = lane & 15, shift = fr & 8 ? 3 : 0;
+  const uint32_t fo = (uint32_t)(fr * 64 + (XQ ? 16 * (g ^ shift) : (g >> 1) * 1024 + 16 * ((2 * (g & 1)) ^ shift)));
+  const uint32_t fo1 = XQ ? fo : fo ^ 16u;
 
   f32x4 acc[R][T];
 #pragma unroll
@@ -249,10 +268,10 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
           static_for<k * kCopies / N, (k + 1) * kCopies / N>(
               [&](auto ic) __attribute__((always_inline)) { copy_one(c0 + D, other, ic); });
       };
-      if constexpr (XQ) {
+      if constexpr (KIND == kCodes) {
         // 2 T steps of one operand and its R products; operands and their scales
         // are read a step ahead, a product's sum is taken kLag products later
-        constexpr int kLag = R > 1 ? 2 : 1, kRing = kLag + 1;
+        constexpr int kLag = R > 2 ? 3 : 1, kRing = kLag + 1;
         const uint8_t* xe = xb + cur + D * kStage + i * kScales + fr * 8;
         u32x4 b[2][2];
         float sx[2], s0[2], s1[2];
@@ -260,8 +279,8 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
         auto read_b = [&](auto kc) __attribute__((always_inline)) {
           constexpr int k = decltype(kc)::value, q = k / T, t = k % T;
           if constexpr (k < 2 * T) {
-            b[k & 1][0] = *(const u32x4*)(xs + t * (16 * kStageBytes) + fo[2 * q]);
-            b[k & 1][1] = *(const u32x4*)(xs + t * (16 * kStageBytes) + fo[2 * q + 1]);
+            b[k & 1][0] = *(const u32x4*)(xs + fo + (4 * t + 2 * q) * 1024);
+            b[k & 1][1] = *(const u32x4*)(xs + fo + (4 * t + 2 * q + 1) * 1024);
             sx[k & 1] = *(const float*)(xe + t * 128 + 4 * q);
           }
         };
@@ -279,6 +298,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
             constexpr int r = decltype(rc)::value, m = k * R + r;
             P[m % kRing] = mfma_e4m3(w[i][r][2 * q], w[i][r][2 * q + 1], b[k & 1][0], b[k & 1][1]);
             take(std::integral_constant<int, m - kLag>{});
+            __builtin_amdgcn_sched_barrier(0);
           });
           copies(kc, std::integral_constant<int, (T >= 2 ? T / 2 : 1)>{});
           if constexpr (t == T - 1) {  // refill what this unit was the last to read
@@ -292,49 +312,77 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
         static_for<2 * T * R - kLag, 2 * T * R>(take);
         if constexpr (!kSpread) load_scales(sl, c + D);
       } else {
-        // T steps of four operands and their 4 R products, whose sums are taken
-        // in the next step; the unit's weights are widened first, so that their
-        // registers are free for the loads of stage c + D
-        bf16x8 A[4][R];
+        // A unit goes in parts of QS operands (the whole one, or halves where the
+        // registers are needed for sums: two vector instructions to a product
+        // instead of one), each part in T steps of QS operands and their QS R
+        // products, whose sums are taken in the next step.  The part's weights are
+        // widened first, so that their registers are free for the loads of stage c + D.
+        constexpr int QS = R * T >= 32 ? 2 : 4, kParts = NU * 4 / QS;
+        constexpr int kFirst = T >= 4 ? T / 4 : 1;  // steps that the copies are spread over
+        constexpr int kPieces = XQ ? QS / 2 : QS;   // 16-byte pieces of an operand row in LDS
+        const uint8_t* xe = xb + cur + D * kStage + i * kScales + fr * 8;
+        u32x4 b[2][kPieces];
+        float sx[2];
+        auto read_b = [&](auto kc) __attribute__((always_inline)) {
+          constexpr int k = decltype(kc)::value, part = k / T, t = k % T, q0 = part * QS;  // q0: of 4 NU operands
+          if constexpr (k < kParts * T) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const u32x4& v = w[i][r][q >> 1];
-            A[q][r] = q & 1 ? fp8x8_to_bf16(v.z, v.w) : fp8x8_to_bf16(v.x, v.y);
+            for (int q = 0; q < kPieces; ++q)
+              b[k & 1][q] = XQ ? *(const u32x4*)(xs + fo + (4 * t + q0 / 2 + q) * 1024)
+                               : *(const u32x4*)(xs + ((q0 + q) & 1 ? fo1 : fo) + (4 * t + ((q0 + q) & 2)) * 1024);
+            if constexpr (XQ) sx[k & 1] = *(const float*)(xe + t * 128 + 4 * (q0 / 4));
           }
-        u32x4 b[2][4];
-        f32x4 P[R];
-        auto read_b = [&](auto tc) __attribute__((always_inline)) {
-          constexpr int t = decltype(tc)::value;
-          if constexpr (t < T)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) b[t & 1][q] = *(const u32x4*)(xs + t * (16 * kStageBytes) + fo[q]);
         };
         read_b(std::integral_constant<int, 0>{});
-        constexpr int kFirst = T >= 4 ? T / 4 : 1;  // steps that the copies are spread over
-        static_for<0, T>([&](auto tc) __attribute__((always_inline)) {
-          constexpr int t = decltype(tc)::value;
-          read_b(std::integral_constant<int, t + 1>{});
-          static_for<0, 4>([&](auto qc) __attribute__((always_inline)) {
-            constexpr int q = decltype(qc)::value;
+        static_for<0, kParts>([&](auto pc) __attribute__((always_inline)) {
+          constexpr int part = decltype(pc)::value, h0 = part * QS / 2, u = h0 / 2;  // h0: of 2 NU halves
+          bf16x8 A[QS][R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if constexpr (q == 0 && t > 0) add(acc[r][t - 1], P[r], sw[i][0], sw[i][1]);
-              P[r] = mfma_bf16(A[q][r], as_bf16x8(b[t & 1][q]), q == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : P[r]);
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int q = 0; q < QS; ++q) {
+              const u32x4& v = w[i][r][h0 + (q >> 1)];
+              A[q][r] = q & 1 ? fp8x8_to_bf16(v.z, v.w) : fp8x8_to_bf16(v.x, v.y);
             }
-          });
-          copies(tc, std::integral_constant<int, kFirst>{});
-          if constexpr (t == kFirst - 1) {
-            static_for<0, NL>([&](auto hc) __attribute__((always_inline)) {
+          f32x4 P[R];
+          float s0 = sw[i][2 * u], s1 = sw[i][2 * u + 1];
+          static_for<0, T>([&](auto tc) __attribute__((always_inline)) {
+            constexpr int t = decltype(tc)::value, k = part * T + t;
+            read_b(std::integral_constant<int, k + 1>{});
+            bf16x8 B[QS];
 #pragma unroll
-              for (int r = 0; r < R; ++r) load_w(sl, r, decltype(hc)::value, c + D);
+            for (int q = 0; q < QS; ++q) {
+              if constexpr (XQ) {
+                const u32x4& v = b[k & 1][q >> 1];
+                B[q] = q & 1 ? fp8x8_to_bf16(v.z, v.w) : fp8x8_to_bf16(v.x, v.y);
+              } else {
+                B[q] = as_bf16x8(b[k & 1][q]);
+              }
+            }
+            static_for<0, QS>([&](auto qc) __attribute__((always_inline)) {
+              constexpr int q = decltype(qc)::value;
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                if constexpr (q == 0 && t > 0) add(acc[r][t - 1], P[r], s0, s1);
+                P[r] = mfma_bf16(A[q][r], B[q], q == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : P[r]);
+              }
             });
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        });
+            if constexpr (XQ) {
+              s0 = sx[k & 1] * sw[i][2 * u];
+              s1 = sx[k & 1] * sw[i][2 * u + 1];
+            }
+            if constexpr (part == 0) copies(tc, std::integral_constant<int, kFirst>{});
+            if constexpr (t == kFirst - 1) {
+              static_for<0, QS / 2>([&](auto hc) __attribute__((always_inline)) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) add(acc[r][T - 1], P[r], sw[i][0], sw[i][1]);
+                for (int r = 0; r < R; ++r) load_w(sl, r, h0 + decltype(hc)::value, c + D);
+              });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          });
+#pragma unroll
+          for (int r = 0; r < R; ++r) add(acc[r][T - 1], P[r], s0, s1);
+        });
         if constexpr (!kSpread) load_scales(sl, c + D);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -342,8 +390,10 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
     // the other buffer has landed and this one's reads are done
     ready(std::integral_constant<int, kYoung>{});
     if constexpr (kSpread) {
+      // the wave's scales are the same in every lane: scalar registers
 #pragma unroll
-      for (int k = 0; k < 2 * NU; ++k) sw[0][k] = sw[1][k];
+      for (int k = 0; k < 2 * NU; ++k)
+        sw[0][k] = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(sw[1][k])));
     }
     cur = kBuf - cur;
   }
@@ -353,58 +403,48 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
   finish<R, T>(d, a, p, acc, xb + wave * kPartLds<R>, s, rg, j, rt0, row0, cnt, &last_flag);
 }
 
-template <bool XQ, int NW, int R, int T, int D, int WPS>
+template <int KIND, int NW, int R, int T, int D, int WPS>
 hipError_t launch_k(const Fp8bDesc& d, const Fp8bArgs& a, const ExpertsPlan& p, hipStream_t s) {
   const unsigned grid = grid_of(d, p, NW * R, NW * 64);
   if (!grid) return hipErrorInvalidValue;
-  fp8b_kernel<XQ, NW, R, T, D, WPS><<<grid, NW * 64, 0, s>>>(d, a, p);
+  fp8b_kernel<KIND, NW, R, T, D, WPS><<<grid, NW * 64, 0, s>>>(d, a, p);
   return hipGetLastError();
 }
 
+constexpr ExpertsShape kShapes[3][8] = {
+#define SPENSE_FP8B_SHAPE(i, nw, r, t, dd, wps) {nw, r, t, dd},
+    {SPENSE_FP8B_BF16_CONFIGS(SPENSE_FP8B_SHAPE)},
+    {SPENSE_FP8B_CODES_CONFIGS(SPENSE_FP8B_SHAPE)},
+    {SPENSE_FP8B_WIDE_CONFIGS(SPENSE_FP8B_SHAPE)},
+#undef SPENSE_FP8B_SHAPE
+};
+
 }  // namespace
 
-int fp8b_config_count(bool codes) {
+int fp8b_config_count(Fp8bKind kind) {
   int n = 0;
-#define SPENSE_FP8B_COUNT(i, nw, r, t, dd, wps) ++n;
-  if (codes) {
-    SPENSE_FP8B_CODES_CONFIGS(SPENSE_FP8B_COUNT)
-  } else {
-    SPENSE_FP8B_BF16_CONFIGS(SPENSE_FP8B_COUNT)
-  }
-#undef SPENSE_FP8B_COUNT
+  while (n < 8 && kShapes[kind][n].waves) ++n;
   return n;
 }
 
-ExpertsShape fp8b_shape(bool codes, int config) {
-#define SPENSE_FP8B_SHAPE(i, nw, r, t, dd, wps) \
-  if (config == i) return ExpertsShape{nw, r, t, dd};
-  if (codes) {
-    SPENSE_FP8B_CODES_CONFIGS(SPENSE_FP8B_SHAPE)
-  } else {
-    SPENSE_FP8B_BF16_CONFIGS(SPENSE_FP8B_SHAPE)
-  }
-#undef SPENSE_FP8B_SHAPE
-  return ExpertsShape{0, 0, 0, 0};
-}
+ExpertsShape fp8b_shape(Fp8bKind kind, int config) { return kShapes[kind][config]; }
 
 hipError_t launch_fp8b_linear(const Fp8bDesc& d, const Fp8bArgs& a, const ExpertsPlan& p, hipStream_t s) {
-#define SPENSE_FP8B_CASE(xq, i, nw, r, t, dd, wps) \
-  case i: return launch_k<xq, nw, r, t, dd, wps>(d, a, p, s);
-  if (a.codes) {
-    switch (p.config) {
-#define SPENSE_FP8B_CODES_CASE(...) SPENSE_FP8B_CASE(true, __VA_ARGS__)
-      SPENSE_FP8B_CODES_CONFIGS(SPENSE_FP8B_CODES_CASE)
-#undef SPENSE_FP8B_CODES_CASE
-    }
-  } else {
-    switch (p.config) {
-#define SPENSE_FP8B_BF16_CASE(...) SPENSE_FP8B_CASE(false, __VA_ARGS__)
-      SPENSE_FP8B_BF16_CONFIGS(SPENSE_FP8B_BF16_CASE)
-#undef SPENSE_FP8B_BF16_CASE
-    }
+#define SPENSE_FP8B_CASE(kind, i, nw, r, t, dd, wps) \
+  case 8 * kind + i: return launch_k<kind, nw, r, t, dd, wps>(d, a, p, s);
+#define SPENSE_FP8B_BF16_CASE(...) SPENSE_FP8B_CASE(kBf16, __VA_ARGS__)
+#define SPENSE_FP8B_CODES_CASE(...) SPENSE_FP8B_CASE(kCodes, __VA_ARGS__)
+#define SPENSE_FP8B_WIDE_CASE(...) SPENSE_FP8B_CASE(kWide, __VA_ARGS__)
+  switch (8 * a.kind + p.config) {
+    SPENSE_FP8B_BF16_CONFIGS(SPENSE_FP8B_BF16_CASE)
+    SPENSE_FP8B_CODES_CONFIGS(SPENSE_FP8B_CODES_CASE)
+    SPENSE_FP8B_WIDE_CONFIGS(SPENSE_FP8B_WIDE_CASE)
+    default: return hipErrorInvalidValue;
   }
+#undef SPENSE_FP8B_WIDE_CASE
+#undef SPENSE_FP8B_CODES_CASE
+#undef SPENSE_FP8B_BF16_CASE
 #undef SPENSE_FP8B_CASE
-  return hipErrorInvalidValue;
 }
 
 }  // namespace spense
