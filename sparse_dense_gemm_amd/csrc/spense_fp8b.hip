@@ -16,7 +16,7 @@ constexpr int kLanes = kFp8Block / 8;  // lanes of a block's row, eight columns 
 // each; the maximum travels over them by row rotations.
 // PADDED: the product kernel's activations (codes 0 from K to whole units).
 // Bound by memory: a lane reads 16 bytes of bf16 (2 x 16 of fp32), writes eight.
-template <typename XT, bool PADDED>
+template <typename XT, bool PADDED, bool STREAM>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const XT* X, int64_t M, int64_t K, int64_t ldx,
                                                             const int32_t* rows, int64_t R, uint8_t* codes,
                                                             int64_t ldc, float* scales, int64_t lds, uint32_t blocks) {
@@ -32,14 +32,14 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const XT* X, int64_t
   const u32x2 c = codes8(v, s);
   uint8_t* out = codes + (int64_t)row * ldc;
   if constexpr (PADDED) *(u32x2*)(out + k) = c;
-  else store_codes8(out, k, K, c);
+  else store_codes8<STREAM>(out, k, K, c);
   if (id % kLanes == 0) scales[(int64_t)row * lds + col] = s;
 }
 
 // A scale for 128 rows x 128 columns: a workgroup takes a block, a wave four of
 // its rows at a time, so that the block is read once and kept in registers while
 // its maximum goes through LDS.
-template <typename XT>
+template <typename XT, bool STREAM>
 __global__ __launch_bounds__(256) void quantize_blocks_kernel(const XT* X, int64_t M, int64_t K, int64_t ldx,
                                                               uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
                                                               uint32_t blocks) {
@@ -76,12 +76,12 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const XT* X, int64
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int64_t r = r0 + 16 * i;
-    if (r < M) store_codes8(codes + r * ldc, k, K, codes8(v[i], s));
+    if (r < M) store_codes8<STREAM>(codes + r * ldc, k, K, codes8(v[i], s));
   }
 }
 
 // Eight columns a thread: one store of 16 bytes of bf16 (two of fp32).  Bound by memory.
-template <typename YT>
+template <typename YT, bool STREAM>
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, int64_t ldc, const float* scales,
                                                          int64_t lds, int rows, int64_t M, int64_t K, YT* Y,
                                                          int64_t ldy) {
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, i
     v[4 * h + 2] = b.x * s;
     v[4 * h + 3] = b.y * s;
   }
-  store_row8<YT>(Y + row * ldy, k, K, v);
+  store_row8<STREAM>(Y + row * ldy, k, K, v);
 }
 
 // Codes and scales that are there already as the product kernel reads them:
@@ -204,59 +204,69 @@ hipError_t by_rows(int64_t rows, int64_t threads_per_row, F&& f) {
   return hipSuccess;
 }
 
-template <typename XT>
+template <bool PADDED, bool STREAM, typename XT>
 void quantize_rows(const XT* X, int64_t M, int64_t K, int64_t ldx, const int32_t* rows, int64_t R, uint8_t* codes,
-                   int64_t ldc, float* scales, int64_t lds, bool padded, hipStream_t s) {
+                   int64_t ldc, float* scales, int64_t lds, hipStream_t s) {
   const int64_t blocks = (K + kFp8Block - 1) / kFp8Block;
-  auto k = padded ? quantize_rows_kernel<XT, true> : quantize_rows_kernel<XT, false>;
-  k<<<groups_of(R * blocks * kLanes), 256, 0, s>>>(X, M, K, ldx, rows, R, codes, ldc, scales, lds, (uint32_t)blocks);
+  quantize_rows_kernel<XT, PADDED, STREAM><<<groups_of(R * blocks * kLanes), 256, 0, s>>>(
+      X, M, K, ldx, rows, R, codes, ldc, scales, lds, (uint32_t)blocks);
+}
+
+template <bool STREAM, typename XT>
+hipError_t quantize(const XT* X, int64_t M, int64_t K, int64_t ldx, int rows, uint8_t* codes, int64_t ldc,
+                    float* scales, int64_t lds, hipStream_t s) {
+  const int64_t blocks = (K + kFp8Block - 1) / kFp8Block;
+  if (rows == 1)
+    return by_rows(M, blocks * kLanes, [&](int64_t r0, int64_t n) {
+      quantize_rows<false, STREAM>(X + r0 * ldx, n, K, ldx, nullptr, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, s);
+    });
+  return by_rows((M + rows - 1) / rows, blocks * 256, [&](int64_t b0, int64_t n) {
+    const int64_t r0 = b0 * rows, m = M - r0 < n * rows ? M - r0 : n * rows;
+    quantize_blocks_kernel<XT, STREAM><<<(unsigned)(n * blocks), 256, 0, s>>>(
+        X + r0 * ldx, m, K, ldx, codes + r0 * ldc, ldc, scales + b0 * lds, lds, (uint32_t)blocks);
+  });
+}
+
+template <bool STREAM, typename YT>
+hipError_t dequantize(const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds, int rows, int64_t M,
+                      int64_t K, YT* Y, int64_t ldy, hipStream_t s) {
+  const int64_t per = (K + 7) / 8;
+  // runs of whole blocks of rows
+  return by_rows((M + kFp8Block - 1) / kFp8Block, per * kFp8Block, [&](int64_t b0, int64_t n) {
+    const int64_t r0 = b0 * kFp8Block, m = M - r0 < n * kFp8Block ? M - r0 : n * kFp8Block;
+    dequantize_kernel<YT, STREAM><<<groups_of(m * per), 256, 0, s>>>(codes + r0 * ldc, ldc, scales + r0 / rows * lds, lds,
+                                                                     rows, m, K, Y + r0 * ldy, ldy);
+  });
 }
 
 }  // namespace
 
 hipError_t launch_fp8b_quantize(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t ldx, int rows,
                                 uint8_t* codes, int64_t ldc, float* scales, int64_t lds, hipStream_t s) {
-  const int64_t blocks = (K + kFp8Block - 1) / kFp8Block;
-  const bool f32 = xdtype == DT_F32;
-  if (rows == 1)
-    return by_rows(M, blocks * kLanes, [&](int64_t r0, int64_t n) {
-      if (f32) quantize_rows((const float*)X + r0 * ldx, n, K, ldx, nullptr, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, false, s);
-      else quantize_rows((const uint16_t*)X + r0 * ldx, n, K, ldx, nullptr, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, false, s);
-    });
-  return by_rows((M + rows - 1) / rows, blocks * 256, [&](int64_t b0, int64_t n) {
-    const int64_t r0 = b0 * rows, m = M - r0 < n * rows ? M - r0 : n * rows;
-    const unsigned grid = (unsigned)(n * blocks);
-    if (f32)
-      quantize_blocks_kernel<float><<<grid, 256, 0, s>>>((const float*)X + r0 * ldx, m, K, ldx, codes + r0 * ldc, ldc,
-                                                         scales + b0 * lds, lds, (uint32_t)blocks);
-    else
-      quantize_blocks_kernel<uint16_t><<<grid, 256, 0, s>>>((const uint16_t*)X + r0 * ldx, m, K, ldx, codes + r0 * ldc,
-                                                            ldc, scales + b0 * lds, lds, (uint32_t)blocks);
-  });
+  const bool stream = M * K > kStreamBytes;
+  if (xdtype == DT_F32)
+    return stream ? quantize<true>((const float*)X, M, K, ldx, rows, codes, ldc, scales, lds, s)
+                  : quantize<false>((const float*)X, M, K, ldx, rows, codes, ldc, scales, lds, s);
+  return stream ? quantize<true>((const uint16_t*)X, M, K, ldx, rows, codes, ldc, scales, lds, s)
+                : quantize<false>((const uint16_t*)X, M, K, ldx, rows, codes, ldc, scales, lds, s);
 }
 
 hipError_t launch_fp8b_dequantize(const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds, int rows,
                                   int64_t M, int64_t K, void* Y, int32_t ydtype, int64_t ldy, hipStream_t s) {
-  const int64_t per = (K + 7) / 8;
-  // runs of whole blocks of rows
-  return by_rows((M + kFp8Block - 1) / kFp8Block, per * kFp8Block, [&](int64_t b0, int64_t n) {
-    const int64_t r0 = b0 * kFp8Block, m = M - r0 < n * kFp8Block ? M - r0 : n * kFp8Block;
-    const float* sc = scales + r0 / rows * lds;
-    if (ydtype == DT_F32)
-      dequantize_kernel<float><<<groups_of(m * per), 256, 0, s>>>(codes + r0 * ldc, ldc, sc, lds, rows, m, K,
-                                                                  (float*)Y + r0 * ldy, ldy);
-    else
-      dequantize_kernel<uint16_t><<<groups_of(m * per), 256, 0, s>>>(codes + r0 * ldc, ldc, sc, lds, rows, m, K,
-                                                                     (uint16_t*)Y + r0 * ldy, ldy);
-  });
+  const bool f32 = ydtype == DT_F32, stream = M * K * (f32 ? 4 : 2) > kStreamBytes;
+  if (f32)
+    return stream ? dequantize<true>(codes, ldc, scales, lds, rows, M, K, (float*)Y, ldy, s)
+                  : dequantize<false>(codes, ldc, scales, lds, rows, M, K, (float*)Y, ldy, s);
+  return stream ? dequantize<true>(codes, ldc, scales, lds, rows, M, K, (uint16_t*)Y, ldy, s)
+                : dequantize<false>(codes, ldc, scales, lds, rows, M, K, (uint16_t*)Y, ldy, s);
 }
 
 hipError_t launch_fp8b_activations(const void* X, int64_t M, int64_t K, int64_t ldx, const int32_t* rows, int64_t R,
                                    uint8_t* codes, int64_t ldc, float* scales, int64_t lds, hipStream_t s) {
   return by_rows(R, (K + kFp8Block - 1) / kFp8Block * kLanes, [&](int64_t r0, int64_t n) {
     // rows picked by index keep X's origin
-    quantize_rows((const uint16_t*)X + (rows ? 0 : r0 * ldx), rows ? M : n, K, ldx, rows ? rows + r0 : nullptr, n,
-                  codes + r0 * ldc, ldc, scales + r0 * lds, lds, true, s);
+    quantize_rows<true, false>((const uint16_t*)X + (rows ? 0 : r0 * ldx), rows ? M : n, K, ldx,
+                               rows ? rows + r0 : nullptr, n, codes + r0 * ldc, ldc, scales + r0 * lds, lds, s);
   });
 }
 

@@ -6,6 +6,8 @@
 //
 // r goes out rounded once, y (from the unrounded r) as fp32, bf16 or e4m3 codes
 // with a scale for each block of 128 columns.
+//
+// One launch reads and writes every operand once.
 #include <algorithm>
 
 #include "spense_fp8b_device.h"
@@ -15,68 +17,193 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 
-// Sum over the workgroup, in a fixed order: over the lanes of a wave, then over
-// the waves.  tmp: 16 floats of LDS that no other sum in flight uses.
+
+// Sum over the lanes of a row of sixteen, then over the wave, in every lane.
+__device__ __forceinline__ float row_sum(float v) {
+  auto add = [&](int o) { v += __int_as_float(o); };
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xF, 0xF, false));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)) +
+         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16)) +
+         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)) +
+         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+}
+
+// Sum over the workgroup (at most sixteen waves), in a fixed order.  tmp: 16
+// floats of LDS that no other sum in flight uses.
 __device__ __forceinline__ float block_sum(float v, float* tmp) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  v = wave_sum(v);
   const int waves = (int)blockDim.x >> 6;
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < waves; ++i) s += tmp[i];
-  return s;
+  const int i = threadIdx.x & 15;
+  return row_sum(i < waves ? tmp[i] : 0.f);
 }
 
-__device__ __forceinline__ void load_any(const void* p, bool f32, int64_t row, int64_t k, int64_t H, float (&v)[8]) {
-  if (f32) load_row8<float>((const float*)p + row, k, H, v);
-  else load_row8<uint16_t>((const uint16_t*)p + row, k, H, v);
+// 1 / sqrt(s / H + eps): the instruction, within a unit in the last place (eps is a
+// normal number, so the sum is)
+__device__ __forceinline__ float rms_scale(float s, const spense_norm& n) {
+  return __builtin_amdgcn_rsqf(fmaf(s, 1.0f / (float)n.H, n.eps));
 }
 
-// o[k .. k + 7] of row t
-template <typename OT>
-__device__ __forceinline__ void load_o(const spense_norm& n, int64_t t, int64_t k, float (&o)[8]) {
-  if (!n.pos) {
-    load_row8<OT>((const OT*)n.O + t * n.ldo, k, n.H, o);
-    return;
-  }
+// Eight values of a row as they are stored: loads go out together and are widened
+// where they are used (a widening beside its load is a wait for it).
+template <typename XT>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 a;
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const uint16_t* x, int64_t k, int64_t H) {
+    if (WHOLE || k + 8 <= H) {
+      a = *(const u32x4_any*)(x + k);
+    } else {
+      a = u32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int64_t j = 0; j < n.k; ++j) {
-    const int64_t at = n.pos[t * n.k + j];
-    if (at < 0 || at >= n.O_rows) continue;
-    const float w = n.weights[t * n.k + j];
-    float v[8];
-    load_row8<OT>((const OT*)n.O + at * n.ldo, k, n.H, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = fmaf(w, v[i], o[i]);
+      for (int i = 0; i < 8; ++i)
+        if (k + i < H) a[i >> 1] |= (uint32_t)x[k + i] << (16 * (i & 1));
+    }
   }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i & 1 ? a[i >> 1] & 0xFFFF0000u : a[i >> 1] << 16);
+  }
+};
+template <>
+struct Raw<float> {
+  f32x4 a, b;
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const float* x, int64_t k, int64_t H) {
+    if (WHOLE || k + 8 <= H) {
+      a = *(const f32x4_any*)(x + k);
+      b = *(const f32x4_any*)(x + k + 4);
+    } else {
+      a = b = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (k + i < H) (i < 4 ? a : b)[i & 3] = x[k + i];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+};
+// the same of a type known at the call
+struct RawAny {
+  Raw<float> f;
+  Raw<uint16_t> h;
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const void* p, bool f32, int64_t row, int64_t k, int64_t H) {
+    if (f32) f.load<WHOLE>((const float*)p + row, k, H);
+    else h.load<WHOLE>((const uint16_t*)p + row, k, H);
+  }
+  __device__ __forceinline__ void multiply(bool f32, float (&v)[8]) const {
+    if (f32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= f.get(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= h.get(i);
+    }
+  }
+};
+
+// Columns k .. k + 7 of a row's operands.  OT, RT: types of O and of the residual;
+// POS: O's rows are summed over j.  Columns from H on are zeros.
+template <typename OT, typename RT, bool POS, bool WHOLE>
+struct Piece {
+  Raw<OT> o[POS ? 2 : 1];
+  Raw<RT> res;
+  RawAny gate, post, pre;
+  float w[2];
+
+  __device__ __forceinline__ void load_row(const spense_norm& n, int64_t t, int64_t k) {
+    if constexpr (POS) load_two(n, t, k, 0);
+    else o[0].template load<WHOLE>((const OT*)n.O + t * n.ldo, k, n.H);
+    if (n.residual) res.template load<WHOLE>((const RT*)n.residual + t * n.ldr, k, n.H);
+  }
+  // rows j0 and j0 + 1 of the sum over j
+  __device__ __forceinline__ void load_two(const spense_norm& n, int64_t t, int64_t k, int j0) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      w[j] = 0.f;
+      if (j0 + j >= n.k) continue;
+      const int64_t at = n.pos[t * n.k + j0 + j];
+      if (at < 0 || at >= n.O_rows) continue;
+      w[j] = n.weights[t * n.k + j0 + j];
+      o[j].template load<WHOLE>((const OT*)n.O + at * n.ldo, k, n.H);
+    }
+  }
+  __device__ __forceinline__ void load_gate(const spense_norm& n, int64_t t, int64_t k) {
+    if (n.post) post.load<WHOLE>(n.post, n.wtype == DT_F32, 0, k, n.H);
+    if (n.gate) gate.load<WHOLE>(n.gate, n.gtype == DT_F32, t * n.ldg, k, n.H);
+  }
+  __device__ __forceinline__ void load_pre(const spense_norm& n, int64_t k) {
+    if (n.Y && n.pre) pre.load<WHOLE>(n.pre, n.wtype == DT_F32, 0, k, n.H);
+  }
+
+  __device__ __forceinline__ void get_o(const spense_norm& n, int64_t t, int64_t k, float (&v)[8]) {
+    if constexpr (!POS) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = o[0].get(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int j0 = 0;;) {  // in the order of j
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int64_t at = j0 + j < n.k ? n.pos[t * n.k + j0 + j] : -1;
+          if (at < 0 || at >= n.O_rows) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = fmaf(w[j], o[j].get(i), v[i]);
+        }
+        j0 += 2;
+        if (j0 >= n.k) break;
+        load_two(n, t, k, j0);
+      }
+    }
+  }
+  // r from o times `inv` (1 without a norm after the block)
+  __device__ __forceinline__ void get_r(const spense_norm& n, float inv, float (&v)[8]) const {
+    if (n.post) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= inv;
+      post.multiply(n.wtype == DT_F32, v);
+    }
+    if (n.gate) gate.multiply(n.gtype == DT_F32, v);
+    if (n.residual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(n.scale, res.get(i), v[i]);
+    }
+  }
+  __device__ __forceinline__ void get_y(const spense_norm& n, float inv, float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    if (n.pre) pre.multiply(n.wtype == DT_F32, v);
+  }
+};
+
+template <bool WHOLE, bool STREAM, typename YT>
+__device__ __forceinline__ void put8(const spense_norm& n, YT* y, int64_t k, const float (&v)[8]) {
+  store_row8<STREAM>(y, k, WHOLE ? k + 8 : n.H, v);
 }
 
-// r[k .. k + 7] of row t from the block's output times `inv` (1 without a norm after it)
-template <typename RT>
-__device__ __forceinline__ void sum_r(const spense_norm& n, int64_t t, int64_t k, float inv, const float (&post)[8],
-                                      const float (&res)[8], const float (&gate)[8], float (&o)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float b = o[i];
-    if (n.post) b = b * inv * post[i];
-    if (n.gate) b *= gate[i];
-    o[i] = n.residual ? fmaf(n.scale, res[i], b) : b;
-  }
-}
-
-__device__ __forceinline__ void put_y(const spense_norm& n, int64_t t, int64_t k, const float (&y)[8]) {
+// y out, of all sixteen lanes that share a block (in: columns below H)
+template <bool WHOLE, bool STREAM>
+__device__ __forceinline__ void put_y(const spense_norm& n, int64_t t, int64_t k, bool in, const float (&y)[8]) {
   if (n.ytype == DT_FP8) {
-    const float s = block_scale(row_max(top8(y)));  // sixteen threads to a block
-    if (k >= n.H) return;
-    store_codes8((uint8_t*)n.Y + t * n.ldy, k, n.H, codes8(y, s));
+    const float s = block_scale(row_max(in ? top8(y) : 0u));
+    if (!in) return;
+    uint8_t* out = (uint8_t*)n.Y + t * n.ldy;
+    store_codes8<STREAM>(out, k, WHOLE ? k + 8 : n.H, codes8(y, s));
     if (k % kFp8Block == 0) n.yscales[t * n.lds + k / kFp8Block] = s;
-  } else if (n.ytype == DT_F32) {
-    store_row8<float>((float*)n.Y + t * n.ldy, k, n.H, y);
-  } else {
-    store_row8<uint16_t>((uint16_t*)n.Y + t * n.ldy, k, n.H, y);
+  } else if (in) {
+    if (n.ytype == DT_F32) put8<WHOLE, STREAM>(n, (float*)n.Y + t * n.ldy, k, y);
+    else put8<WHOLE, STREAM>(n, (uint16_t*)n.Y + t * n.ldy, k, y);
   }
 }
 
@@ -88,123 +215,135 @@ __device__ __forceinline__ float sum_of_squares(const float (&v)[8]) {
 }
 
 // A workgroup takes a row, a thread C pieces of eight columns, in registers
-// between the sums.  With up to two pieces the weights' and gates' loads go out
-// with the row's; with four there are no registers for them, and they are loaded
-// where they are used.
-template <typename OT, typename RT, int C>
+// between the sums.
+template <typename OT, typename RT, bool POS, bool WHOLE, bool STREAM, int C>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(spense_norm n) {
   __shared__ float tmp[2][16];
   const int64_t t = blockIdx.x;
   const int64_t step = (int64_t)blockDim.x * 8, k0 = (int64_t)threadIdx.x * 8;
-  constexpr bool kHold = C <= 2;
-  constexpr int CW = kHold ? C : 1;
-  float o[C][8], res[C][8], gate[CW][8], post[CW][8], pre[CW][8];
-  auto load_gate = [&](int64_t k, int c) __attribute__((always_inline)) {
-    if (n.gate) load_any(n.gate, n.gtype == DT_F32, t * n.ldg, k, n.H, gate[c]);
-    if (n.post) load_any(n.post, n.wtype == DT_F32, 0, k, n.H, post[c]);
-  };
-  auto load_pre = [&](int64_t k, int c) __attribute__((always_inline)) {
-    if (n.Y && n.pre) load_any(n.pre, n.wtype == DT_F32, 0, k, n.H, pre[c]);
-  };
+  // several pieces: no registers for the weights and gates, which are loaded where they are used
+  constexpr bool kHold = C == 1;
+  Piece<OT, RT, POS, WHOLE> p[C];
+  float v[C][8];
+  bool in[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int64_t k = k0 + c * step;
-    load_o<OT>(n, t, k, o[c]);
-    if (n.residual) load_row8<RT>((const RT*)n.residual + t * n.ldr, k, n.H, res[c]);
-    if constexpr (kHold) {
-      load_gate(k, c);
-      load_pre(k, c);
-    }
+    in[c] = k < n.H;
+    if (in[c]) p[c].load_row(n, t, k);
   }
-  float inv = 1.f;
+  if constexpr (kHold) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (in[c]) {
+        p[c].load_gate(n, t, k0 + c * step);
+        p[c].load_pre(n, k0 + c * step);
+      }
+  }
+  float inv = 1.f, s = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (in[c]) p[c].get_o(n, t, k0 + c * step, v[c]);
   if (n.post) {
-    float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) s += sum_of_squares(o[c]);
-    inv = 1.f / sqrtf(block_sum(s, tmp[0]) / (float)n.H + n.eps);
+    for (int c = 0; c < C; ++c)
+      if (in[c]) s += sum_of_squares(v[c]);
+    inv = rms_scale(block_sum(s, tmp[0]), n);
+    s = 0.f;
   }
-  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (in[c]) {
+      const int64_t k = k0 + c * step;
+      if constexpr (!kHold) p[c].load_gate(n, t, k);
+      p[c].get_r(n, inv, v[c]);
+      if (n.residual_out) put8<WHOLE, STREAM>(n, (RT*)n.residual_out + t * n.ldro, k, v[c]);
+      s += sum_of_squares(v[c]);
+    }
+  if (!n.Y) return;
+  inv = rms_scale(block_sum(s, tmp[1]), n);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int64_t k = k0 + c * step;
-    const int w = kHold ? c : 0;
-    if constexpr (!kHold) load_gate(k, 0);
-    sum_r<RT>(n, t, k, inv, post[w], res[c], gate[w], o[c]);
-    if (n.residual_out) store_row8<RT>((RT*)n.residual_out + t * n.ldro, k, n.H, o[c]);
-    s += sum_of_squares(o[c]);
-  }
-  if (!n.Y) return;
-  inv = 1.f / sqrtf(block_sum(s, tmp[1]) / (float)n.H + n.eps);
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int w = kHold ? c : 0;
-    if constexpr (!kHold) load_pre(k0 + c * step, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[c][i] = n.pre ? o[c][i] * inv * pre[w][i] : o[c][i] * inv;
-    put_y(n, t, k0 + c * step, o[c]);
+    if (in[c]) {
+      if constexpr (!kHold) p[c].load_pre(n, k);
+      p[c].get_y(n, inv, v[c]);
+    }
+    put_y<WHOLE, STREAM>(n, t, k, in[c], v[c]);
   }
 }
 
 // Rows that do not fit the registers of a workgroup: read again for each sum.
-template <typename OT, typename RT>
+template <typename OT, typename RT, bool POS, bool STREAM>
 __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(spense_norm n) {
   __shared__ float tmp[2][16];
   const int64_t t = blockIdx.x;
   const int64_t step = (int64_t)blockDim.x * 8, k0 = (int64_t)threadIdx.x * 8;
-  float inv = 1.f;
-  if (n.post) {
-    float s = 0.f;
-    for (int64_t k = k0; k < n.H; k += step) {
-      float o[8];
-      load_o<OT>(n, t, k, o);
-      s += sum_of_squares(o);
-    }
-    inv = 1.f / sqrtf(block_sum(s, tmp[0]) / (float)n.H + n.eps);
-  }
-  auto r_of = [&](int64_t k, float(&o)[8]) {
-    float res[8], gate[8], post[8];
-    load_o<OT>(n, t, k, o);
-    if (n.residual) load_row8<RT>((const RT*)n.residual + t * n.ldr, k, n.H, res);
-    if (n.gate) load_any(n.gate, n.gtype == DT_F32, t * n.ldg, k, n.H, gate);
-    if (n.post) load_any(n.post, n.wtype == DT_F32, 0, k, n.H, post);
-    sum_r<RT>(n, t, k, inv, post, res, gate, o);
+  float inv = 1.f, inv2 = 1.f, s = 0.f;
+  Piece<OT, RT, POS, false> p;
+  float v[8];
+  auto get_r = [&](int64_t k) __attribute__((always_inline)) {
+    p.load_row(n, t, k);
+    p.load_gate(n, t, k);
+    p.get_o(n, t, k, v);
+    p.get_r(n, inv, v);
   };
-  float inv2 = 1.f;
-  if (n.Y) {
-    float s = 0.f;
+  if (n.post) {
     for (int64_t k = k0; k < n.H; k += step) {
-      float o[8];
-      r_of(k, o);
-      s += sum_of_squares(o);
+      p.load_row(n, t, k);
+      p.get_o(n, t, k, v);
+      s += sum_of_squares(v);
     }
-    inv2 = 1.f / sqrtf(block_sum(s, tmp[1]) / (float)n.H + n.eps);
+    inv = rms_scale(block_sum(s, tmp[0]), n);
+    s = 0.f;
   }
-  // every thread of a row of sixteen lanes takes part in a block's maximum; a
-  // thread writes what it alone has read (residual_out may be residual)
+  if (n.Y) {
+    for (int64_t k = k0; k < n.H; k += step) {
+      get_r(k);
+      s += sum_of_squares(v);
+    }
+    inv2 = rms_scale(block_sum(s, tmp[1]), n);
+  }
+  // every lane takes part in a block's maximum; a thread writes what it alone has
+  // read (residual_out may be residual)
   for (int64_t kb = 0; kb < n.H; kb += step) {
     const int64_t k = kb + k0;
-    float o[8];
-    r_of(k, o);
-    if (n.residual_out) store_row8<RT>((RT*)n.residual_out + t * n.ldro, k, n.H, o);
+    const bool in = k < n.H;
+    if (in) {
+      get_r(k);
+      if (n.residual_out) put8<false, STREAM>(n, (RT*)n.residual_out + t * n.ldro, k, v);
+    }
     if (!n.Y) continue;
-    float pre[8];
-    if (n.pre) load_any(n.pre, n.wtype == DT_F32, 0, k, n.H, pre);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = n.pre ? o[i] * inv2 * pre[i] : o[i] * inv2;
-    put_y(n, t, k, o);
+    if (in) {
+      p.load_pre(n, k);
+      p.get_y(n, inv2, v);
+    }
+    put_y<false, STREAM>(n, t, k, in, v);
   }
 }
 
-template <typename OT, typename RT>
+template <typename OT, typename RT, bool POS, bool STREAM>
 hipError_t launch(const spense_norm& n, hipStream_t s) {
   const unsigned T = (unsigned)n.T;
   const int64_t pieces = (n.H + 7) / 8;
+  const bool whole = n.H % 8 == 0;
   auto threads = [&](int64_t c) { return (unsigned)(((pieces + c - 1) / c + 63) / 64 * 64); };
-  if (pieces <= kMaxThreads) norm_kernel<OT, RT, 1><<<T, threads(1), 0, s>>>(n);
-  else if (pieces <= 2 * kMaxThreads) norm_kernel<OT, RT, 2><<<T, threads(2), 0, s>>>(n);
-  else if (pieces <= 4 * kMaxThreads) norm_kernel<OT, RT, 4><<<T, threads(4), 0, s>>>(n);
-  else norm_long_kernel<OT, RT><<<T, kMaxThreads, 0, s>>>(n);
+  if (pieces <= kMaxThreads) {
+    auto k = whole ? norm_kernel<OT, RT, POS, true, STREAM, 1> : norm_kernel<OT, RT, POS, false, STREAM, 1>;
+    k<<<T, threads(1), 0, s>>>(n);
+  } else if (pieces <= 4 * kMaxThreads) {
+    auto k = whole ? norm_kernel<OT, RT, POS, true, STREAM, 4> : norm_kernel<OT, RT, POS, false, STREAM, 4>;
+    k<<<T, threads(4), 0, s>>>(n);
+  } else {
+    norm_long_kernel<OT, RT, POS, STREAM><<<T, kMaxThreads, 0, s>>>(n);
+  }
   return hipGetLastError();
+}
+
+template <typename OT, typename RT>
+hipError_t launch_types(const spense_norm& n, bool stream, hipStream_t s) {
+  if (n.pos) return stream ? launch<OT, RT, true, true>(n, s) : launch<OT, RT, true, false>(n, s);
+  return stream ? launch<OT, RT, false, true>(n, s) : launch<OT, RT, false, false>(n, s);
 }
 
 }  // namespace
@@ -213,6 +352,8 @@ hipError_t launch_block_norm(const spense_norm& n, hipStream_t s) {
   // a launch's grid counts threads in 32 bits
   constexpr int64_t kMost = (int64_t(1) << 30) / kMaxThreads;
   auto bytes = [](int32_t t) { return t == DT_F32 ? 4 : t == DT_BF16 ? 2 : 1; };
+  const int64_t per = (n.residual_out ? bytes(n.rtype) : 0) + (n.Y ? bytes(n.ytype) : 0);
+  const bool stream = n.T * n.H * per > kStreamBytes, r32 = n.rtype == DT_F32;
   for (int64_t t0 = 0; t0 < n.T; t0 += kMost) {
     spense_norm m = n;
     m.T = std::min(n.T - t0, kMost);
@@ -227,9 +368,10 @@ hipError_t launch_block_norm(const spense_norm& n, hipStream_t s) {
     if (n.residual_out) m.residual_out = (uint8_t*)n.residual_out + t0 * n.ldro * bytes(n.rtype);
     if (n.Y) m.Y = (uint8_t*)n.Y + t0 * n.ldy * bytes(n.ytype);
     if (n.yscales) m.yscales += t0 * n.lds;
-    hipError_t e;
-    if (n.otype == DT_F32) e = n.rtype == DT_F32 ? launch<float, float>(m, s) : launch<float, uint16_t>(m, s);
-    else e = n.rtype == DT_F32 ? launch<uint16_t, float>(m, s) : launch<uint16_t, uint16_t>(m, s);
+    const hipError_t e =
+        n.otype == DT_F32
+            ? (r32 ? launch_types<float, float>(m, stream, s) : launch_types<float, uint16_t>(m, stream, s))
+            : (r32 ? launch_types<uint16_t, float>(m, stream, s) : launch_types<uint16_t, uint16_t>(m, stream, s));
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
