@@ -435,7 +435,8 @@ int spense_pack_experts(const void* W, int32_t wdtype, const uint8_t* scales, in
  *
  *   X        device pointer, [M, ldx] bf16, ldx >= K, 1 <= M <= 2^24 (M = 0 only with R = 0).
  *   adtype   SPENSE_BF16: the activations as they are; SPENSE_MX4: quantised in the
- *            call (mx4 weights only).
+ *            call (mx4 weights only); SPENSE_FP8_E4M3: the same for fp8b weights
+ *            (spense_pack_experts_fp8b).
  *   rows     device pointer, [R] int32 rows of X, or NULL (then M >= R); a row
  *            outside [0, M) is taken as zeros.
  *   offsets  device pointer, [E + 1] int32, ascending from 0 on; values past R count as R.
@@ -622,7 +623,7 @@ typedef struct spense_norm {
   int32_t k;                 /* with pos: 1 <= k <= 1024 */
   int32_t otype, wtype, gtype, rtype; /* SPENSE_F32 or SPENSE_BF16 */
   int32_t ytype;             /* SPENSE_F32, SPENSE_BF16 or SPENSE_FP8_E4M3 */
-  float scale, eps;          /* finite scale; eps > 0 */
+  float scale, eps;          /* finite scale; finite eps >= 2^-126 */
 } spense_norm;
 
 /*

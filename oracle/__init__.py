@@ -40,10 +40,11 @@ written from the definitions on the pages:
     four consecutive weights.
 
 The microscaled 4-bit format, the experts' layers and the router
-(``experts.py``) are not on the pages; they are written from their formulas.
+(``experts.py``), the block-scaled 8-bit format and the pass between two blocks
+(``fp8b.py``) are not on the pages; they are written from their formulas.
 
-Parity status: every function is pinned by ``tests/test_oracle.py`` or
-``tests/test_experts_oracle.py`` (closed forms, exhaustive brute force on tiny
+Parity status: every function is pinned by ``tests/test_oracle.py``,
+``tests/test_experts_oracle.py`` or ``tests/test_fp8b_oracle.py`` (closed forms, exhaustive brute force on tiny
 inputs, library routines for the special cases).  No function is "parity
 unpinned".
 """
@@ -56,6 +57,15 @@ from .experts import (  # noqa: F401
     nearest_e2m1,
     product_ref,
     route_ref,
+)
+from .fp8b import (  # noqa: F401
+    block_norm_ref,
+    dropped_bits_ref,
+    e4m3_values,
+    fp8b_expert_values_ref,
+    fp8b_quantize_ref,
+    fp8b_values_ref,
+    nearest_e4m3,
 )
 from .spense import (  # noqa: F401
     DT_BF16,

@@ -297,7 +297,7 @@ int spense_experts_linear_fp8b(spense_handle h, const uint8_t* codes, int64_t ld
 int spense_block_norm(const spense_norm* n, void* stream) {
   if (!n || n->T < 0 || n->T > kMaxRows || n->H < 1 || n->H > kMaxColumns) return SPENSE_EINVAL;
   if (!n->Y && !n->residual_out) return SPENSE_EINVAL;
-  if (!(n->eps > 0.f) || !finite(n->eps) || !finite(n->scale)) return SPENSE_EINVAL;
+  if (!(n->eps >= 1.17549435e-38f) || !finite(n->eps) || !finite(n->scale)) return SPENSE_EINVAL;  // a normal number
   if (!n->pos != !n->weights) return SPENSE_EINVAL;
   if (n->pos && (n->k < 1 || n->k > kMaxExperts || n->O_rows < 0 || n->O_rows > kMaxRows)) return SPENSE_EINVAL;
   if (n->T > 0 && !n->O && !(n->pos && n->O_rows == 0)) return SPENSE_EINVAL;
