@@ -296,7 +296,7 @@ int spense_experts_linear_fp8b(spense_handle h, const uint8_t* codes, int64_t ld
 
 int spense_block_norm(const spense_norm* n, void* stream) {
   if (!n || n->T < 0 || n->T > kMaxRows || n->H < 1 || n->H > kMaxColumns) return SPENSE_EINVAL;
-  if (!n->Y && !n->residual_out) return SPENSE_EINVAL;
+  if (n->T > 0 && !n->Y && !n->residual_out) return SPENSE_EINVAL;
   if (!(n->eps >= 1.17549435e-38f) || !finite(n->eps) || !finite(n->scale)) return SPENSE_EINVAL;  // a normal number
   if (!n->pos != !n->weights) return SPENSE_EINVAL;
   if (n->pos && (n->k < 1 || n->k > kMaxExperts || n->O_rows < 0 || n->O_rows > kMaxRows)) return SPENSE_EINVAL;
@@ -305,7 +305,8 @@ int spense_block_norm(const spense_norm* n, void* stream) {
   if (n->ldo < n->H || (n->gate && n->ldg != 0 && n->ldg < n->H) || (n->residual && n->ldr < n->H) ||
       (n->residual_out && n->ldro < n->H) || (n->Y && n->ldy < n->H))
     return SPENSE_EINVAL;
-  if (codes ? !n->yscales || n->lds < (n->H + kFp8Block - 1) / kFp8Block : n->yscales != nullptr) return SPENSE_EINVAL;
+  if (codes ? (n->T > 0 && !n->yscales) || n->lds < (n->H + kFp8Block - 1) / kFp8Block : n->yscales != nullptr)
+    return SPENSE_EINVAL;
   if (n->residual && n->residual == n->residual_out && n->ldr != n->ldro) return SPENSE_EINVAL;
   const struct {
     bool used;

@@ -86,7 +86,8 @@ def norm(**kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(), OK), (dict(T=-1), EINVAL), (dict(T=BIG), EINVAL), (dict(H=0), EINVAL), (dict(H=(1 << 20) + 1), EINVAL),
-    (dict(T=1, O=None), EINVAL), (dict(Y=None, residual_out=None), EINVAL), (dict(eps=0.0), EINVAL),
+    (dict(T=1, O=None), EINVAL), (dict(T=1, Y=None, residual_out=None), EINVAL),
+    (dict(Y=None, residual_out=None), OK), (dict(eps=0.0), EINVAL),
     (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(eps=float("inf")), EINVAL),
     (dict(eps=1e-40), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(scale=float("nan")), EINVAL),
     (dict(ldo=299), EINVAL), (dict(ldg=299), EINVAL), (dict(ldg=-300), EINVAL), (dict(ldr=299), EINVAL),
@@ -95,7 +96,7 @@ def norm(**kw):
     (dict(pos=P), EINVAL), (dict(weights=P), EINVAL), (dict(pos=P, weights=P, k=0), EINVAL),
     (dict(pos=P, weights=P, k=1025), EINVAL), (dict(pos=P, weights=P, k=2, O_rows=-1), EINVAL),
     (dict(pos=P, weights=P, k=2, O_rows=BIG), EINVAL), (dict(pos=P, weights=P, k=2), OK),
-    (dict(yscales=P), EINVAL), (dict(ytype=FP8), EINVAL), (dict(ytype=FP8, yscales=P, lds=2), EINVAL),
+    (dict(yscales=P), EINVAL), (dict(T=1, ytype=FP8), EINVAL), (dict(ytype=FP8), EINVAL), (dict(ytype=FP8, yscales=P, lds=2), EINVAL),
     (dict(ytype=FP8, yscales=P, lds=3), OK), (dict(otype=FP8), EUNSUP), (dict(otype=7), EINVAL),
     (dict(wtype=MX4), EUNSUP), (dict(gtype=FP8), EUNSUP), (dict(rtype=FP8), EUNSUP), (dict(ytype=MX4), EUNSUP),
     (dict(gate=None, gtype=9, ldg=-5), OK), (dict(residual=None, ldr=0), OK), (dict(Y=None, ldy=0, ytype=9), OK),
