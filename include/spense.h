@@ -558,7 +558,7 @@ int spense_pack_fp8b(const uint8_t* codes, int64_t ldc, const float* scales, int
  * strides at least its own (rows of codes that do not start at 16 bytes, or a K
  * that is no multiple of 16, and rows of bf16 that do not start at 16 bytes, or a
  * K that is no multiple of 8, are laid out in the workspace first, and so are
- * rows 2^22 or more elements apart).
+ * rows of bf16 2^22 or more elements apart and scales 2^21 or more apart).
  */
 int spense_linear_fp8b(spense_handle h, const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds, int64_t M,
                        void* Y, int32_t ydtype, int64_t ldy, void* stream);

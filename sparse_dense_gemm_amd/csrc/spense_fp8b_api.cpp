@@ -81,8 +81,8 @@ struct Fp8bLayer final : GroupedLayer {
   int64_t weight_bytes = 0, device_bytes = 0;
   ProductWorkspaces w;
   // rows that the partial sums and counters have been sized for, whatever split
-  // count a smaller call's plan takes: [kind][grouped]
-  int64_t sized[3][2] = {{0, 0}, {0, 0}, {0, 0}};
+  // count a smaller call's plan takes and, with codes, whatever Y's type: [codes][grouped]
+  int64_t sized[2][2] = {{0, 0}, {0, 0}};
 
   ~Fp8bLayer() override {
     if (d.wpack) (void)hipFree(d.wpack);
@@ -146,9 +146,14 @@ struct Fp8bLayer final : GroupedLayer {
     const int64_t n_rows = rows && !gather ? M : R;
     const int64_t codes_bytes = codes ? align256(n_rows * a.ldx) : 0;
     if (prepare) need.xws = codes ? codes_bytes + n_rows * a.ldxs : n_rows * a.ldx;
-    int64_t& have = sized[kind][grouped];
+    int64_t& have = sized[codes][grouped];
     if (R > have) {  // every smaller call too: none of them may allocate later (graph capture)
-      for (int64_t r = (have / 16 + 1) * 16; r < R; r += 16) need.grow(plan_need(d, make_plan(d, grouped, r, kind), r));
+      auto size = [&](int64_t r, Fp8bKind k) { need.grow(plan_need(d, make_plan(d, grouped, r, k), r)); };
+      for (int64_t r = (have / 16 + 1) * 16; r < R + 16; r += 16) {
+        const int64_t at = std::min(r, R);
+        size(at, codes ? kCodes : kBf16);
+        if (codes) size(at, kWide);
+      }
     }
     if (!w.fits(need)) {
       const int rc = w.grow(need, s);
