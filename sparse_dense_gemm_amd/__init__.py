@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import numpy as np
@@ -118,20 +119,6 @@ def _lib():
     lib.spense_route.restype = ctypes.c_int
     lib.spense_experts_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i32, i64, vp]
     lib.spense_experts_combine.restype = ctypes.c_int
-    lib.spense_quantize_fp8b.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, i64, vp]
-    lib.spense_quantize_fp8b.restype = ctypes.c_int
-    lib.spense_dequantize_fp8b.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, vp]
-    lib.spense_dequantize_fp8b.restype = ctypes.c_int
-    lib.spense_pack_fp8b.argtypes = [vp, i64, vp, i64, i64, i64, vp, ctypes.POINTER(vp)]
-    lib.spense_pack_fp8b.restype = ctypes.c_int
-    lib.spense_linear_fp8b.argtypes = [vp, vp, i64, vp, i64, i64, vp, i32, i64, vp]
-    lib.spense_linear_fp8b.restype = ctypes.c_int
-    lib.spense_pack_experts_fp8b.argtypes = [vp, vp, i64, i64, i64, i64, i64, i32, vp, ctypes.POINTER(vp)]
-    lib.spense_pack_experts_fp8b.restype = ctypes.c_int
-    lib.spense_experts_linear_fp8b.argtypes = [vp, vp, i64, vp, i64, i64, vp, vp, i64, vp, i32, i64, vp]
-    lib.spense_experts_linear_fp8b.restype = ctypes.c_int
-    lib.spense_block_norm.argtypes = [ctypes.POINTER(NormCall), vp]
-    lib.spense_block_norm.restype = ctypes.c_int
     lib.spense_info.argtypes = [vp, ctypes.POINTER(LayerInfo)]
     lib.spense_info.restype = ctypes.c_int
     lib.spense_export.argtypes = [vp, vp, vp, vp, vp, vp, vp]
@@ -144,8 +131,28 @@ def _lib():
     lib.spense_last_hip_error.restype = ctypes.c_int
     lib.spense_abi_version.argtypes = []
     lib.spense_abi_version.restype = ctypes.c_int
+    if hasattr(lib, "spense_quantize_fp8b"):  # a build without spense_fp8b_api.cpp has none of them
+        _declare_fp8b(lib)
     _lib_handle = lib
     return lib
+
+
+def _declare_fp8b(lib) -> None:
+    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    lib.spense_quantize_fp8b.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, i64, vp]
+    lib.spense_quantize_fp8b.restype = ctypes.c_int
+    lib.spense_dequantize_fp8b.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, vp]
+    lib.spense_dequantize_fp8b.restype = ctypes.c_int
+    lib.spense_pack_fp8b.argtypes = [vp, i64, vp, i64, i64, i64, vp, ctypes.POINTER(vp)]
+    lib.spense_pack_fp8b.restype = ctypes.c_int
+    lib.spense_linear_fp8b.argtypes = [vp, vp, i64, vp, i64, i64, vp, i32, i64, vp]
+    lib.spense_linear_fp8b.restype = ctypes.c_int
+    lib.spense_pack_experts_fp8b.argtypes = [vp, vp, i64, i64, i64, i64, i64, i32, vp, ctypes.POINTER(vp)]
+    lib.spense_pack_experts_fp8b.restype = ctypes.c_int
+    lib.spense_experts_linear_fp8b.argtypes = [vp, vp, i64, vp, i64, i64, vp, vp, i64, vp, i32, i64, vp]
+    lib.spense_experts_linear_fp8b.restype = ctypes.c_int
+    lib.spense_block_norm.argtypes = [vp, vp]  # a spense_norm
+    lib.spense_block_norm.restype = ctypes.c_int
 
 
 def _check(status: int, where: str):
@@ -603,19 +610,15 @@ def spense_experts_combine(O, pos, weights, Y, *, stream=None) -> None:
 FP8B_BLOCK = 128
 
 
-def _need_codes(t, what: str) -> None:
-    if t.element_size() != 1:
-        raise TypeError(f"{what} are bytes (uint8 or float8_e4m3fn), not {t.dtype}")
-
-
 def _fp8b_strides(codes, scales, M: int, K: int, rows: int):
     """Row strides of an fp8b matrix of at least M x K, its blocks `rows` rows high."""
     crows, ccols, ldc = _matrix(codes, "codes")
     srows, scols, lds = _matrix(scales, "scales")
-    _need_codes(codes, "codes")
+    if codes.element_size() != 1:
+        raise TypeError(f"codes are bytes (uint8 or float8_e4m3fn), not {codes.dtype}")
     if scales.dtype is not _torch().float32:
         _need_dtype(scales, _torch().float32, "scales")
-    if crows < M or ccols < K or srows < -(-M // rows) or scols < -(-K // FP8B_BLOCK):
+    if crows < M or ccols < K or srows * rows < M or scols * FP8B_BLOCK < K:
         raise ValueError(f"codes {crows} x {ccols} and scales {srows} x {scols} do not hold {M} x {K} fp8b")
     return ldc, lds
 
@@ -715,11 +718,28 @@ def _experts_linear_fp8b(h, dims, codes, scales, offsets, Y, rows, R, stream):
     _check(st, "spense_experts_linear_fp8b")
 
 
-def _norm_matrix(t, rows: int, H: int, what: str):
-    r, c, ld = _matrix(t, what)
-    if r < rows or c < H:
+# spense_norm in one packing: a third of the time of a ctypes structure's fields
+_NORM = struct.Struct("=19q6i2f")
+
+
+def _operand(t, rows: int, H: int, what: str):
+    """Address, row stride and type of a matrix that holds at least rows x H values."""
+    have, cols = t.shape
+    ld, step = t.stride()
+    if have < rows or cols < H:
         _too_small(what, rows, H)
-    return t.data_ptr(), ld
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} {have} x {cols} is not contiguous along a row")
+    d = _dtypes.get(t.dtype)
+    return t.data_ptr(), ld, dtype_of(t) if d is None else d
+
+
+def _vector(t, H: int, what: str):
+    """Address and type of H contiguous values."""
+    if t.numel() < H or not t.is_contiguous():
+        _need_flat(t, t.dtype, H, what)
+    d = _dtypes.get(t.dtype)
+    return t.data_ptr(), dtype_of(t) if d is None else d
 
 
 def spense_block_norm(O, residual, residual_out, Y, *, pre=None, post=None, gate=None, eps: float, scale: float = 1.0,
@@ -727,55 +747,54 @@ def spense_block_norm(O, residual, residual_out, Y, *, pre=None, post=None, gate
     """The pass over the rows between two blocks: o = O, or sum_j weights[t, j] O[pos[t, j]];
     r = scale * residual + gate * (post: rms(o) * post, else o) into residual_out, rms(r) * pre into Y.
 
-    residual, residual_out and Y may be None (zeros; not stored), residual_out may be residual.  gate is [T, H], or [1, H] or
-    [H] for all rows.  With yscales (float32 [T, ceil(H / 128)]) Y holds bytes and receives fp8b codes."""
-    torch = _torch()
-    orows, H, ldo = _matrix(O, "O")
-    T = orows
-    kk = 0
+    residual, residual_out and Y may be None (zeros; not stored), residual_out may be residual.  gate is [T, H], or
+    [1, H] or [H] for all rows.  With yscales (float32 [T, ceil(H / 128)]) Y holds bytes and receives fp8b codes."""
+    T, H = O.shape
+    O_p, ldo, otype = _operand(O, 0, H, "O")
+    orows, k, pos_p, weights_p = T, 0, 0, 0
     if pos is not None:
-        T, kk = pos.shape
-        _need_flat(pos, torch.int32, 0, "pos")
+        T, k = pos.shape
+        _need_flat(pos, _torch().int32, 0, "pos")
         if weights is None:
             raise ValueError("pos needs weights")
-        _need_flat(weights, torch.float32, T * kk, "weights")
+        _need_flat(weights, _torch().float32, T * k, "weights")
+        pos_p, weights_p = pos.data_ptr(), weights.data_ptr()
     elif weights is not None:
         raise ValueError("weights need pos")
-    wtype = gtype = rtype = ytype = 0
-    post_p = pre_p = gate_p = res_p = out_p = y_p = ys_p = None
-    ldg = ldr = ldro = ldy = lds = 0
-    for w in (post, pre):
-        if w is not None:
-            _need_flat(w, w.dtype, H, "post and pre")
-            wtype = dtype_of(w)
-    if post is not None and pre is not None and post.dtype is not pre.dtype:
-        raise TypeError(f"post is {post.dtype}, pre {pre.dtype}")
-    post_p, pre_p = _ptr(post), _ptr(pre)
+    post_p = pre_p = gate_p = res_p = out_p = y_p = ys_p = 0
+    ldg = ldr = ldro = ldy = lds = wtype = gtype = rtype = ytype = 0
+    if post is not None:
+        post_p, wtype = _vector(post, H, "post")
+    if pre is not None:
+        pre_p, w = _vector(pre, H, "pre")
+        if post is not None and w != wtype:
+            raise TypeError(f"post is {post.dtype}, pre {pre.dtype}")
+        wtype = w
     if gate is not None:
-        gtype = dtype_of(gate)
         if gate.dim() == 1 or gate.shape[0] == 1:
-            _need_flat(gate, gate.dtype, H, "gate")
-            gate_p = gate.data_ptr()
+            gate_p, gtype = _vector(gate, H, "gate")
         else:
-            gate_p, ldg = _norm_matrix(gate, T, H, "gate")
+            gate_p, ldg, gtype = _operand(gate, T, H, "gate")
     if residual is not None:
-        rtype = dtype_of(residual)
-        res_p, ldr = _norm_matrix(residual, T, H, "residual")
+        res_p, ldr, rtype = _operand(residual, T, H, "residual")
     if residual_out is not None:
-        if residual is not None and residual_out.dtype is not residual.dtype:
+        out_p, ldro, r = _operand(residual_out, T, H, "residual_out")
+        if residual is not None and r != rtype:
             raise TypeError(f"residual is {residual.dtype}, residual_out {residual_out.dtype}")
-        rtype = dtype_of(residual_out)
-        out_p, ldro = _norm_matrix(residual_out, T, H, "residual_out")
+        rtype = r
     if Y is not None:
         if yscales is not None:
             ldy, lds = _fp8b_strides(Y, yscales, T, H, 1)
             y_p, ys_p, ytype = Y.data_ptr(), yscales.data_ptr(), DT_FP8
         else:
-            ytype = dtype_of(Y)
-            y_p, ldy = _norm_matrix(Y, T, H, "Y")
-    call = NormCall(T, H, O.data_ptr(), ldo, orows, _ptr(pos), _ptr(weights), post_p, pre_p, gate_p, ldg, res_p, ldr,
-                    out_p, ldro, y_p, ldy, ys_p, lds, kk, dtype_of(O), wtype, gtype, rtype, ytype, scale, eps)
-    _check(_lib().spense_block_norm(ctypes.byref(call), _stream(stream)), "spense_block_norm")
+            y_p, ldy, ytype = _operand(Y, T, H, "Y")
+    elif yscales is not None:
+        raise ValueError("yscales need Y")
+    call = _NORM.pack(T, H, O_p, ldo, orows, pos_p, weights_p, post_p, pre_p, gate_p, ldg, res_p, ldr, out_p, ldro, y_p,
+                      ldy, ys_p, lds, k, otype, wtype, gtype, rtype, ytype, scale, eps)
+    st = _lib().spense_block_norm(call, _stream(stream))
+    if st != SPENSE_OK:
+        _check(st, "spense_block_norm")
 
 
 def spense_info(h: int) -> dict:

@@ -106,6 +106,12 @@ def test_block_norm_rejects(kw, want):
     assert norm(**kw) == want
 
 
+def test_packed_call_is_the_structure():
+    """The binding's packing of a call has the bytes of the C structure."""
+    values = (*range(1, 26), 0.5, 0.25)
+    assert bytes(sdg.NormCall(*values)) == sdg._NORM.pack(*values)
+
+
 def test_block_norm_null():
     assert sdg._lib().spense_block_norm(None, None) == EINVAL
 
