@@ -36,6 +36,7 @@ enum Fp8bKind : int32_t { kBf16 = 0, kCodes = 1, kWide = 2 };
 
 struct Fp8bArgs : ExpertsArgs {  // X: bf16 rows, or codes with scales at xs (row stride ldxs bytes)
   Fp8bKind kind;
+  int32_t stream;                // 1: weights with the non-temporal hint (configurations of fewer than 8 m-tiles)
 };
 
 // The configurations of spense_fp8b_linear.hip.

@@ -67,6 +67,20 @@ ExpertsPlan make_plan(const Fp8bDesc& d, bool grouped, int64_t R, Fp8bKind kind)
       "SPENSE_FP8B");
 }
 
+// Whether a launch's weights are streamed past the caches: where one m-group reads
+// them (of experts' rows, which come in any number, where an average expert fills
+// half of one), and they are more than a last-level cache that other layers share
+// could keep.  us, default and streamed, layers in turn: 131 MB at one row 27.2
+// and 23.4, at 29 rows 32.9 and 29.0, at 64 rows 35.9 and 33.5; 262 MB of 16
+// experts, 128 rows 56.5 and 48.4, but 512 rows (two m-groups to some) 76 and 92;
+// 66 MB at one row 14.0 and 15.5.
+bool stream_weights(const Fp8bDesc& d, bool grouped, int64_t R, const ExpertsShape& c) {
+  constexpr int64_t kKept = int64_t(96) << 20;
+  const int64_t hit = grouped ? std::min(d.E, R) : 1;
+  if (hit * d.NT * d.tile_bytes <= kKept) return false;
+  return grouped && d.E > 1 ? R <= 8 * c.t * hit : R <= 16 * c.t;
+}
+
 // The activations of a call: bf16, or codes with their scales.
 struct Activations {
   const void* X;
@@ -120,6 +134,7 @@ struct Fp8bLayer final : GroupedLayer {
     a.ldy = ldy;
     a.ydtype = ydtype;
     a.kind = kind;
+    a.stream = stream_weights(d, grouped, R, fp8b_shape(kind, p.config));
     // The product kernel reads rows of 16-byte pieces through offsets of 31
     // bits: activations are quantised into that form, or read in place if they
     // have it and laid out first if not: the R rows that are read, gathered if

@@ -67,7 +67,8 @@ __device__ __forceinline__ f32x4 mfma_e4m3(const u32x4& a0, const u32x4& a1, con
                                                           f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-template <int KIND, int NW, int R, int T, int D, int WPS>
+// POL: cache policy of the weights' loads
+template <int KIND, int NW, int R, int T, int D, int WPS, int POL>
 __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs a, ExpertsPlan p) {
   constexpr bool XQ = KIND != kBf16;                     // activations are codes
   constexpr int kRows = 16 * T;
@@ -76,12 +77,13 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
   constexpr uint32_t kScales = XQ ? kRows * 8u : 0u;     // and their scales: [row][unit]
   constexpr uint32_t kBuf = D * (kStage + kScales);
   constexpr int NL = 2 * NU;                             // 16-byte weight loads per row tile and stage
-  constexpr int kLoads = R * NL + 1;                     // with the weights' scales: loads per wave and stage
+  constexpr bool kSpread = D == 1;
+  constexpr int kLoads = R * NL + (kSpread ? 0 : 1);     // with the weights' scales: vector loads per wave and stage
   constexpr int kWait = D * kLoads;                      // and of the whole ring
   static_assert(kWait < 64, "the wait fits the counter");
-  // With one stage in the ring its copies are spread over the first products,
-  // and its scales are loaded a stage ahead.
-  constexpr bool kSpread = D == 1;
+  // With one stage in the ring its copies are spread over the first products, and
+  // its weights' scales, the same in every lane, are loaded a stage ahead into
+  // scalar registers.
   constexpr int kYoung = kSpread ? R * NL : kWait;       // weight loads after the last copy
   __shared__ __attribute__((aligned(1024))) uint8_t xb[2 * kBuf];
   __shared__ int last_flag;
@@ -112,8 +114,8 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
   const __amdgpu_buffer_rsrc_t wr =
       make_rsrc(d.wpack + ((int64_t)e * d.NT + (nrt ? rt0 : 0)) * d.tile_bytes, (uint32_t)(nrt * d.tile_bytes));
   static_assert(8 % R == 0, "a wave's row tiles share their scales");
-  const __amdgpu_buffer_rsrc_t sr =
-      make_rsrc(d.scales + ((int64_t)e * d.SG + (nrt ? rt0 / 8 : 0)) * d.NUe * 2, (uint32_t)(d.NUe * 8));
+  const float* scales = d.scales + ((int64_t)e * d.SG + (nrt ? rt0 / 8 : 0)) * d.NUe * 2;
+  const __amdgpu_buffer_rsrc_t sr = make_rsrc(scales, (uint32_t)(d.NUe * 8));
   const uint32_t tb = (uint32_t)d.tile_bytes;
   u32x4 w[D][R][NL];
   float sw[kSpread ? 2 : D][2 * NU];  // [unit][even, odd packed rows]
@@ -124,19 +126,26 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
     const int st = lo + c;
     const bool in = c < n && (!XQ || i < 2 || 2 * st + 1 < (int)d.NU);
     const uint32_t at = in ? (uint32_t)st * (NL * 1024u) : kOutOfRange;
-    w[decltype(slot)::value][r][i] = buf_load16(wr, 16 * lane + 1024 * i, at + (uint32_t)r * tb);
+    w[decltype(slot)::value][r][i] = buf_load16<POL>(wr, 16 * lane + 1024 * i, at + (uint32_t)r * tb);
   };
   auto load_scales = [&](auto slot, int c) __attribute__((always_inline)) {
-    const uint32_t off = c < n ? (uint32_t)(lo + c) * (8u * NU) : kOutOfRange;
     float(&o)[2 * NU] = sw[decltype(slot)::value];
-    if constexpr (XQ) {
-      const f32x4 v = __builtin_bit_cast(f32x4, buf_load16(sr, 0, off));
+    if constexpr (kSpread) {  // past the last stage the last one's again
+      typedef const __attribute__((address_space(4))) float* Scalar;
+      const Scalar p = (Scalar)(uintptr_t)(scales + (int64_t)(lo + (c < n ? c : n - 1)) * (2 * NU));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = v[i];
+      for (int i = 0; i < 2 * NU; ++i) o[i] = p[i];
     } else {
-      const f32x2 v = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(sr, 0, (int)off, 0));
-      o[0] = v.x;
-      o[1] = v.y;
+      const uint32_t off = c < n ? (uint32_t)(lo + c) * (8u * NU) : kOutOfRange;
+      if constexpr (XQ) {
+        const f32x4 v = __builtin_bit_cast(f32x4, buf_load16(sr, 0, off));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = v[i];
+      } else {
+        const f32x2 v = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(sr, 0, (int)off, 0));
+        o[0] = v.x;
+        o[1] = v.y;
+      }
     }
   };
 
@@ -390,10 +399,8 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
     // the other buffer has landed and this one's reads are done
     ready(std::integral_constant<int, kYoung>{});
     if constexpr (kSpread) {
-      // the wave's scales are the same in every lane: scalar registers
 #pragma unroll
-      for (int k = 0; k < 2 * NU; ++k)
-        sw[0][k] = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(sw[1][k])));
+      for (int k = 0; k < 2 * NU; ++k) sw[0][k] = sw[1][k];
     }
     cur = kBuf - cur;
   }
@@ -407,7 +414,13 @@ template <int KIND, int NW, int R, int T, int D, int WPS>
 hipError_t launch_k(const Fp8bDesc& d, const Fp8bArgs& a, const ExpertsPlan& p, hipStream_t s) {
   const unsigned grid = grid_of(d, p, NW * R, NW * 64);
   if (!grid) return hipErrorInvalidValue;
-  fp8b_kernel<KIND, NW, R, T, D, WPS><<<grid, NW * 64, 0, s>>>(d, a, p);
+  if constexpr (T < 8) {
+    if (a.stream) {
+      fp8b_kernel<KIND, NW, R, T, D, WPS, kNonTemporal><<<grid, NW * 64, 0, s>>>(d, a, p);
+      return hipGetLastError();
+    }
+  }
+  fp8b_kernel<KIND, NW, R, T, D, WPS, 0><<<grid, NW * 64, 0, s>>>(d, a, p);
   return hipGetLastError();
 }
 

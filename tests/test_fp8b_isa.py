@@ -33,7 +33,7 @@ def kernels(tmp_path_factory):
         if m:
             end = labels[i + 1][0] if i + 1 < len(labels) else len(text)
             found[m.group(1)] = text[pos:end].splitlines()
-    assert len(found) == 14  # five configurations of the bf16 and codes kinds, four of the widened codes
+    assert len(found) == 23  # five configurations of the bf16 and codes kinds, four of the widened codes; nine of them streamed too
     return found
 
 
