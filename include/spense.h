@@ -598,8 +598,9 @@ int spense_experts_linear_fp8b(spense_handle h, const uint8_t* codes, int64_t ld
  *   r[t]  = scale * residual[t] + gate[t] * b[t]
  *   y[t]  = rms(r[t]) * pre
  *
- * in fp32 throughout; r is rounded once into residual_out, y once into Y, from the
- * unrounded r.
+ * in fp32 throughout (squares that sum to 2^128 or more make an infinite mean, and
+ * the normalised row 0); r is rounded once into residual_out, y once into Y, from
+ * the unrounded r.
  */
 typedef struct spense_norm {
   int64_t T, H;              /* rows and columns: 0 <= T <= 2^24, 1 <= H <= 2^20 */

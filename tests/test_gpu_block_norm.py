@@ -219,6 +219,22 @@ def test_zero_rows_and_non_finite_values():
     assert ys[4].isnan().all() and (Y[4] == 0).all()  # 0 * inf in the norm after the block
 
 
+def test_sums_of_squares_out_of_range():
+    """Squares beyond the range of fp32: the mean is infinite and the normalised row 0, as in the formula."""
+    T, H = 3, 256
+    d = tensors(T, H, 11, post=False)
+    d["O"][1] = 1e25
+    R2, Y, _ = run(d, "f32", "f32", T, H)
+    assert (R2[1] == fma(d, 1)).all() and (Y[1] == 0).all()
+    r, want, dr, dy = reference({k: (v[[0, 2]] if v.dim() == 2 else v) for k, v in d.items()}, 0.75)
+    assert_close(f64(Y[[0, 2]]), want, dy, "rows beside it")
+
+
+def fma(d, t):
+    """0.75 * residual + O rounded once."""
+    return dev((0.75 * f64(d["residual"][t]) + f64(d["O"][t])).astype(np.float32))
+
+
 def test_many_rows():
     """More rows than a wave of workgroups, streamed results: sampled rows."""
     T, H = 8191, 5120
