@@ -550,7 +550,7 @@ int spense_pack_fp8b(const uint8_t* codes, int64_t ldc, const float* scales, int
  *
  *   codes, scales  device pointers, [M, ldc] e4m3 codes, ldc >= K, and [M, lds]
  *            float32, lds >= ceil(K / 128), for example from spense_quantize_fp8b
- *            or spense_block_norm.
+ *            or spense_block_norm.  ldc, lds < 2^23 (SPENSE_EUNSUPPORTED).
  *   Y        device pointer, [M, ldy] of ydtype (SPENSE_F32 or SPENSE_BF16), ldy >= N.
  * 1 <= M <= 2^24.  Deterministic; workspaces, asynchrony and graph capture as for
  * spense_linear on such a layer: a captured call needs an eager one of the same
@@ -628,8 +628,9 @@ typedef struct spense_norm {
 } spense_norm;
 
 /*
- * One launch, asynchronous on `stream`, graph-capturable, no state kept.  Besides
- * residual_out as residual, no output may overlap an input or another output.
+ * One launch to 2^20 rows, asynchronous on `stream`, graph-capturable, no state
+ * kept.  Besides residual_out as residual, no output may overlap an input or
+ * another output (SPENSE_EINVAL where they start at the same address).
  * Types of operands that are NULL are ignored.  Deterministic.
  */
 int spense_block_norm(const spense_norm* n, void* stream);

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void pack_scales_kernel(Fp8bDesc d, int64_t g0
 unsigned groups_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
 
 // A launch's grid counts threads in 32 bits: f(first row, rows) over runs of
-// rows of at most 2^30 threads (a row takes at most 2^20).
+// rows of at most 2^30 threads (a row takes at most 2^24).
 template <typename F>
 hipError_t by_rows(int64_t rows, int64_t threads_per_row, F&& f) {
   const int64_t most = (int64_t(1) << 30) / threads_per_row;

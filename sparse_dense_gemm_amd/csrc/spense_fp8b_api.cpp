@@ -250,7 +250,7 @@ int quantized_call(spense_handle h, const uint8_t* codes, int64_t ldc, const flo
   const Fp8bDesc& d = g->d;
   if (ldc < d.K || lds < d.NU || ldy < (d.glu ? d.N / 2 : d.N)) return SPENSE_EINVAL;
   if (float_status(ydtype) != SPENSE_OK) return float_status(ydtype);
-  if (ldc >= kMaxLd) return SPENSE_EUNSUPPORTED;
+  if (ldc >= kMaxLd || lds >= kMaxLd) return SPENSE_EUNSUPPORTED;
   if (R == 0) return SPENSE_OK;
   return g->call(Activations{codes, ldc, scales, lds, false}, M, rows, offsets, R, Y, ydtype, ldy, (hipStream_t)stream);
 }
@@ -328,6 +328,11 @@ int spense_block_norm(const spense_norm* n, void* stream) {
   if (codes ? (n->T > 0 && !n->yscales) || n->lds < (n->H + kFp8Block - 1) / kFp8Block : n->yscales != nullptr)
     return SPENSE_EINVAL;
   if (n->residual && n->residual == n->residual_out && n->ldr != n->ldro) return SPENSE_EINVAL;
+  if (n->T > 0) {  // a row is read by several sums, and picked rows by several workgroups
+    for (const void* in : {n->O, n->post, n->pre, n->gate})
+      if (in && (in == n->residual_out || in == n->Y)) return SPENSE_EINVAL;
+    if (n->Y && (n->Y == n->residual || n->Y == n->residual_out)) return SPENSE_EINVAL;
+  }
   const struct {
     bool used;
     int32_t type;

@@ -106,6 +106,16 @@ def test_block_norm_rejects(kw, want):
     assert norm(**kw) == want
 
 
+OTHER = {name: P + (i << 16) for i, name in enumerate(("O", "post", "pre", "gate", "residual", "residual_out", "Y"))}
+
+
+@pytest.mark.parametrize("out,into", [("Y", "O"), ("Y", "post"), ("Y", "pre"), ("Y", "gate"), ("Y", "residual"),
+                                      ("Y", "residual_out"), ("residual_out", "O"), ("residual_out", "gate")])
+def test_block_norm_refuses_outputs_in_place(out, into):
+    assert norm(**{**OTHER, "T": 0, out: OTHER[into]}) == OK
+    assert norm(**{**OTHER, "T": 3, out: OTHER[into]}) == EINVAL
+
+
 def test_packed_call_is_the_structure():
     """The binding's packing of a call has the bytes of the C structure."""
     values = (*range(1, 26), 0.5, 0.25)

@@ -146,6 +146,24 @@ def test_aligned_activations_are_read_in_place(lib):
         lib.spense_free(h)
 
 
+def test_strides_of_scales(lib):
+    """Scales far apart are laid out first; a stride whose products could leave 64 bits is refused."""
+    for kind in ("codes", "experts codes"):
+        h = CALLS[kind][0](lib)
+        for lds, want in (((1 << 21) - 1, True), (1 << 21, False), ((1 << 23) - 1, False)):
+            lib.host_forget8()
+            if kind == "codes":
+                assert lib.spense_linear_fp8b(h, P, K, P, lds, 5, P, F32, N, STREAM) == 0
+            else:
+                assert lib.spense_experts_linear_fp8b(h, P, K, P, lds, 5, None, P, 5, P, F32, N, STREAM) == 0
+            assert (lib.host_seen8(X) == P) == want, (kind, lds)
+        for lds in (1 << 23, 1 << 37, (1 << 62) + 5):
+            st = (lib.spense_linear_fp8b(h, P, K, P, lds, 5, P, F32, N, STREAM) if kind == "codes" else
+                  lib.spense_experts_linear_fp8b(h, P, K, P, lds, 5, None, P, 5, P, F32, N, STREAM))
+            assert st == sdg.SPENSE_EUNSUPPORTED, (kind, lds)
+        lib.spense_free(h)
+
+
 def test_info(lib):
     i = sdg.LayerInfo()
     h = layer(lib)
