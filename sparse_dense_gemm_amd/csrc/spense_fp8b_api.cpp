@@ -27,14 +27,31 @@ bool matrix_ok(int64_t M, int64_t K, int64_t ldc, int64_t lds) {
   return M >= 0 && M <= kMaxRows && K >= 1 && K <= kMaxColumns && ldc >= K && lds >= (K + kFp8Block - 1) / kFp8Block;
 }
 
+constexpr int64_t kKept = int64_t(96) << 20;
+
+// Whether a launch's weights are streamed past the caches (configurations of fewer
+// than 8 m-tiles have that form): where one m-group reads them (of experts' rows,
+// which come in any number, where an average expert fills half of one), and they
+// are more than a last-level cache that other layers share could keep.  us, default
+// and streamed, layers in turn: 131 MB at one row 27.2 and 23.4, at 29 rows 32.9 and
+// 29.0, at 64 rows 35.9 and 33.5; 262 MB of 16 experts, 128 rows 56.5 and 48.4, but
+// 512 rows (two m-groups to some) 76 and 92; 66 MB at one row 14.0 and 15.5.
+bool stream_weights(const Fp8bDesc& d, bool grouped, int64_t R, const ExpertsShape& c) {
+  const int64_t hit = grouped ? std::min(d.E, R) : 1;
+  if (c.t >= 8 || hit * d.NT * d.tile_bytes <= kKept) return false;
+  return grouped && d.E > 1 ? R <= 8 * c.t * hit : R <= 16 * c.t;
+}
+
 // Estimated cycles of a launch of `groups` m-groups.  Per stage (256 bytes of
 // every activation row) a workgroup multiplies and moves its weights and
 // activations through the CU's vector cache at 64 bytes a cycle; a stage takes at
 // least the memory latency over the stages in flight, and the launch the time
-// its weights take from memory.  Two workgroups run together on a CU.  With
-// split K every sum is written and read once more, and a workgroup reads its
-// tile's S sums by itself.
-double plan_cycles(const Fp8bDesc& d, Fp8bKind kind, int config, int64_t S, double groups, int64_t hit, int64_t R) {
+// its weights take from memory, longer where they go through caches that do not
+// keep them (131 MB at 29 rows: 28 us streamed, 36 with two m-groups).  Two
+// workgroups run together on a CU.  With split K every sum is written and read once
+// more, and a workgroup reads its tile's S sums by itself.
+double plan_cycles(const Fp8bDesc& d, bool grouped, Fp8bKind kind, int config, int64_t S, double groups, int64_t hit,
+                   int64_t R) {
   const ExpertsShape c = fp8b_shape(kind, config);
   const bool codes = kind != kBf16;
   const double wkb = (codes ? 4.0 : 2.0) * c.waves * c.r, xkb = 4.0 * c.t;
@@ -49,7 +66,8 @@ double plan_cycles(const Fp8bDesc& d, Fp8bKind kind, int config, int64_t S, doub
     return (double)(load / 2) * std::max(2.0 * w, least) + (load % 2 ? std::max(1.3 * w, least) : 0.0);
   };
   double t = stage(work, latency) * (double)stages + stage(0.5 * work, 0.0) * (double)empty;
-  t = std::max(t, (double)(hit * d.NT * d.tile_bytes) / 2600.0);
+  const int64_t bytes = hit * d.NT * d.tile_bytes;
+  t = std::max(t, (double)bytes / (bytes <= kKept || stream_weights(d, grouped, R, c) ? 2600.0 : 2000.0));
   t += 3000.0 * (double)((load + 1) / 2);
   if (S > 1) {
     const double tile = 1024.0 * c.waves * c.r * c.t;  // bytes of a workgroup's sums
@@ -63,22 +81,8 @@ ExpertsPlan make_plan(const Fp8bDesc& d, bool grouped, int64_t R, Fp8bKind kind)
   return choose_plan(
       d, grouped, R, codes ? (d.NU + 1) / 2 : d.NU, codes ? 2 : 4, fp8b_config_count(kind),
       [&](int i) { return fp8b_shape(kind, i); },
-      [&](int i, int64_t S, double groups, int64_t hit, int64_t R16) { return plan_cycles(d, kind, i, S, groups, hit, R16); },
+      [&](int i, int64_t S, double groups, int64_t hit, int64_t R16) { return plan_cycles(d, grouped, kind, i, S, groups, hit, R16); },
       "SPENSE_FP8B");
-}
-
-// Whether a launch's weights are streamed past the caches: where one m-group reads
-// them (of experts' rows, which come in any number, where an average expert fills
-// half of one), and they are more than a last-level cache that other layers share
-// could keep.  us, default and streamed, layers in turn: 131 MB at one row 27.2
-// and 23.4, at 29 rows 32.9 and 29.0, at 64 rows 35.9 and 33.5; 262 MB of 16
-// experts, 128 rows 56.5 and 48.4, but 512 rows (two m-groups to some) 76 and 92;
-// 66 MB at one row 14.0 and 15.5.
-bool stream_weights(const Fp8bDesc& d, bool grouped, int64_t R, const ExpertsShape& c) {
-  constexpr int64_t kKept = int64_t(96) << 20;
-  const int64_t hit = grouped ? std::min(d.E, R) : 1;
-  if (hit * d.NT * d.tile_bytes <= kKept) return false;
-  return grouped && d.E > 1 ? R <= 8 * c.t * hit : R <= 16 * c.t;
 }
 
 // The activations of a call: bf16, or codes with their scales.

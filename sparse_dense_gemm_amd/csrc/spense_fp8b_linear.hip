@@ -28,6 +28,17 @@
 // each wave's registers through a ring of D stages, activations are copied into
 // LDS, D stages at a time into one of two buffers while the other is read.  A
 // stage is 256 bytes of every row: 128 bf16 columns or 256 codes.
+//
+// What bounds it.  Few rows: the weights' way from memory (25600 x 5120 at one row
+// 23 us, 5120 x 25600 at 29 rows 30 us: 5.6 and 4.5 TB/s).  Many rows of codes:
+// operands from L2 and the matrix units in turn (55296 x 5120, 2048 rows 525 us,
+// 2.2 PFLOP/s: matrix units busy 56% of the cycles, 75% where the loads are taken
+// out, 394 us; 31 bytes a cycle and CU from L2; a plain library product of that size
+// with one scale takes 466).  Many rows of bf16: the vector unit, which issues a
+// 16x16x32 product (12 cycles of its time), two FMAs and half a widening in the 16
+// cycles that the product runs (12288 x 5120, 2048 rows 219 us, 1.18 PFLOP/s; the
+// library's bf16 product 241).  Experts: 16 x 3200 x 5120, 8192 rows of codes 161 us:
+// 936 workgroups, two rounds of the 512 that run at once, where 1.8 would do.
 #include "spense_experts_device.h"
 #include "spense_fp8b.h"
 
@@ -35,8 +46,13 @@ namespace spense {
 namespace {
 
 // Configurations: X(index, waves, row tiles per wave R, m-tiles T, stages D in
-// the ring and in an LDS buffer, waves per SIMD the registers allow)
-// (256 columns of widened codes need more registers than two workgroups have)
+// the ring and in an LDS buffer, waves per SIMD the registers allow).  The fewer
+// m-tiles, the less there is to multiply behind a stage's loads and the more stages
+// are on their way; the more row tiles a wave has, the more products an operand
+// row read from LDS feeds.  us of configurations 0 to 4: 25600 x 5120 bf16 at one row
+// 23, 27, 31, 43, -; 5120 x 25600 codes at 29 rows (fp32 out) 46, 32, 33, 45, -;
+// 55296 x 5120 codes at 2048 rows -, -, 987, 662, 547; 12288 x 5120 bf16 there -, -,
+// 327, 250, 229.
 #define SPENSE_FP8B_CODES_CONFIGS(X) \
   X(0, 8, 1, 1, 8, 2)                \
   X(1, 4, 1, 2, 4, 2)                \
@@ -49,6 +65,7 @@ namespace {
   X(2, 8, 1, 4, 2, 2)               \
   X(3, 4, 2, 8, 1, 2)               \
   X(4, 4, 4, 8, 1, 2)
+// (256 columns of widened codes need more registers than two workgroups have)
 #define SPENSE_FP8B_WIDE_CONFIGS(X) \
   X(0, 8, 1, 1, 8, 2)               \
   X(1, 4, 1, 2, 4, 2)               \
@@ -279,8 +296,11 @@ __global__ __launch_bounds__(NW * 64, WPS) void fp8b_kernel(Fp8bDesc d, Fp8bArgs
       };
       if constexpr (KIND == kCodes) {
         // 2 T steps of one operand and its R products; operands and their scales
-        // are read a step ahead, a product's sum is taken kLag products later
-        constexpr int kLag = R > 2 ? 3 : 1, kRing = kLag + 1;
+        // are read a step ahead, a product's sum is taken kLag products later (55296
+        // x 5120, 2048 rows: R = 4 one later 576 us, two 552, three 545; R = 2 one 678,
+        // two 662)
+        constexpr int kLag = R > 2 ? 3 : R, kRing = kLag + 1;
+        static_assert(kLag <= R, "a sum is taken in its own step or the next, while its scales are there");
         const uint8_t* xe = xb + cur + D * kStage + i * kScales + fr * 8;
         u32x4 b[2][2];
         float sx[2], s0[2], s1[2];

@@ -7,7 +7,12 @@
 // r goes out rounded once, y (from the unrounded r) as fp32, bf16 or e4m3 codes
 // with a scale for each block of 128 columns.
 //
-// One launch reads and writes every operand once.
+// One launch reads and writes every operand once: a workgroup takes a row, which
+// stays in registers between the two sums (a wave a row would hold 80 values a lane
+// at 5120 columns, and few rows would leave the chip empty).  Bound by memory: 8191
+// rows of 5120 (bf16 in, residual and gate in fp32 and bf16, codes out) 99 us, 464 MB
+// at 4.7 TB/s; 2048 rows of 5120, each the sum of two fp32 rows, 28 us, 147 MB at 5.3.
+// One row takes 3.0 us, most of it the launch and the wait for its loads.
 #include <algorithm>
 
 #include "spense_fp8b_device.h"
@@ -16,7 +21,6 @@ namespace spense {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-
 
 // Sum over the lanes of a row of sixteen, then over the wave, in every lane.
 __device__ __forceinline__ float row_sum(float v) {
@@ -222,7 +226,7 @@ __device__ __forceinline__ float sum_of_squares(const float (&v)[8]) {
 }
 
 // A workgroup takes a row, a thread C pieces of eight columns, in registers
-// between the sums.
+// between the sums.  Eight columns are one load of bf16.
 template <typename OT, typename RT, bool POS, bool WHOLE, bool STREAM, int C>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(spense_norm n, float rh) {
   __shared__ float tmp[2][16];
