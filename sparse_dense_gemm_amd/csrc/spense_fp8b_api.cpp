@@ -42,36 +42,55 @@ bool stream_weights(const Fp8bDesc& d, bool grouped, int64_t R, const ExpertsSha
   return grouped && d.E > 1 ? R <= 8 * c.t * hit : R <= 16 * c.t;
 }
 
-// Estimated cycles of a launch of `groups` m-groups.  Per stage (256 bytes of
-// every activation row) a workgroup multiplies and moves its weights and
-// activations through the CU's vector cache at 64 bytes a cycle; a stage takes at
-// least the memory latency over the stages in flight, and the launch the time
-// its weights take from memory, longer where they go through caches that do not
-// keep them (131 MB at 29 rows: 28 us streamed, 36 with two m-groups).  Two
-// workgroups run together on a CU.  With split K every sum is written and read once
-// more, and a workgroup reads its tile's S sums by itself.
+// Estimated time of a launch of `groups` m-groups, in cycles or so.  Per stage (256
+// bytes of every activation row) a workgroup multiplies and moves its weights and
+// activations through the CU's vector cache; a stage takes at least the memory
+// latency over the stages in flight, and the launch the time its weights take from
+// memory, longer where they go through caches that do not keep them (131 MB at 29
+// rows: 28 us streamed, 36 with two m-groups).  Two workgroups run together on a CU.
+// With split K every sum is written and read once more, and a workgroup reads its
+// tile's S sums by itself.  The constants are fitted to the order of 3678 timings
+// (every configuration and split count that a plan may take, three kinds of
+// products, 8 layers of 4 to 131 MB, 1 to 1024 rows): the plan's time is 1.010 of
+// the best one's on average, at worst 1.15.
+// Experts with few rows: fewer of them are hit than may be, in groups of any size,
+// and workgroups of 128 columns then leave CUs idle, or read weights twice where an
+// expert has more rows than they take; those of 64 columns (two m-tiles) spread
+// better.  us of one, two and four m-tiles, gate/up of 16 experts of 3200 x 5120: 26
+// rows of codes 36, 31, 33; 10 with fp32 out 23, 17, 30; 80 rows of codes 48, 36, 40,
+// of bf16 45, 38, 44; of 1600 x 5120, 16 rows of bf16 23, 17, 28.  One m-tile of bf16,
+// of which a CU takes two workgroups, is ahead where there are enough of them and
+// experts have two rows or fewer: 10 rows 23, 27, 29.
 double plan_cycles(const Fp8bDesc& d, bool grouped, Fp8bKind kind, int config, int64_t S, double groups, int64_t hit,
                    int64_t R) {
   const ExpertsShape c = fp8b_shape(kind, config);
-  const bool codes = kind != kBf16;
+  const bool codes = kind != kBf16, few = grouped && d.E > 1 && groups <= (double)hit;
+  if (few) groups *= 0.85;
+  const double product = kind == kBf16 ? 10.4 : kind == kCodes ? 12.0 : 30.0;  // of a row tile and an m-tile
+  const double more = c.t == 1 ? 1.7 : c.t == 2 ? 1.5 : c.t == 4 ? 1.42 : c.r == 2 ? 1.04 : 1.39;
   const double wkb = (codes ? 4.0 : 2.0) * c.waves * c.r, xkb = 4.0 * c.t;
-  const double work = ((kind == kWide ? 32.0 : 16.0) * c.waves * c.r * c.t + 16.0 * (wkb + xkb)) * (c.t < 4 ? 1.3 : c.t == 4 ? 1.45 : 1.0) + 60.0;
-  const double latency = c.stages > 1 ? 3000.0 / c.stages : 2000.0;
+  const double work = (product * c.waves * c.r * c.t + 15.0 * (wkb + xkb)) * more + 75.0;
+  const double latency = c.stages > 1 ? 2400.0 / c.stages : 4150.0;
   const int64_t rg = (d.NT + c.waves * c.r - 1) / (c.waves * c.r);
   const int64_t stages = ((codes ? (d.NU + 1) / 2 : d.NU) + S - 1) / S;
   // a pass takes the ring's stages together; those past the end wait for nothing
   const int64_t empty = (stages + c.stages - 1) / c.stages * c.stages - stages;
   const int64_t load = (int64_t)std::ceil((double)rg * groups * (double)S / kCUs);  // workgroups of the fullest CU
   auto stage = [&](double w, double least) {
-    return (double)(load / 2) * std::max(2.0 * w, least) + (load % 2 ? std::max(1.3 * w, least) : 0.0);
+    return (double)(load / 2) * std::max(2.0 * w, least) + (load % 2 ? std::max(1.04 * w, least) : 0.0);
   };
   double t = stage(work, latency) * (double)stages + stage(0.5 * work, 0.0) * (double)empty;
   const int64_t bytes = hit * d.NT * d.tile_bytes;
-  t = std::max(t, (double)bytes / (bytes <= kKept || stream_weights(d, grouped, R, c) ? 2600.0 : 2000.0));
-  t += 3000.0 * (double)((load + 1) / 2);
+  double memory = (double)bytes / (bytes <= kKept || stream_weights(d, grouped, R, c) ? 3260.0 : 2700.0);
+  if (few) {
+    const bool ahead = kind == kBf16 && R <= 2 * hit && (double)rg * groups >= kCUs;
+    memory *= c.t == 1 && !ahead ? 1.06 : c.t <= 2 ? 0.85 : 0.94;
+  }
+  t = std::max(t, memory);
+  t += 4000.0 * (double)((load + 1) / 2);
   if (S > 1) {
     const double tile = 1024.0 * c.waves * c.r * c.t;  // bytes of a workgroup's sums
-    t += 4000.0 + (double)(S + 1) * tile / 40.0 + (double)(S * d.NT * 16 * R) * 8.0 / 1500.0;
+    t += 4650.0 + (double)(S + 1) * tile / 80.0 + (double)(S * d.NT * 16 * R) * 8.0 / 1165.0;
   }
   return t;
 }
@@ -81,7 +100,9 @@ ExpertsPlan make_plan(const Fp8bDesc& d, bool grouped, int64_t R, Fp8bKind kind)
   return choose_plan(
       d, grouped, R, codes ? (d.NU + 1) / 2 : d.NU, codes ? 2 : 4, fp8b_config_count(kind),
       [&](int i) { return fp8b_shape(kind, i); },
-      [&](int i, int64_t S, double groups, int64_t hit, int64_t R16) { return plan_cycles(d, grouped, kind, i, S, groups, hit, R16); },
+      [&](int i, int64_t S, double groups, int64_t hit, int64_t R16) {
+        return plan_cycles(d, grouped, kind, i, S, groups, hit, R16);
+      },
       "SPENSE_FP8B");
 }
 

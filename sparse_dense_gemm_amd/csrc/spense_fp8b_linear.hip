@@ -36,7 +36,7 @@
 // out, 394 us; 31 bytes a cycle and CU from L2; a plain library product of that size
 // with one scale takes 466).  Many rows of bf16: the vector unit, which issues a
 // 16x16x32 product (12 cycles of its time), two FMAs and half a widening in the 16
-// cycles that the product runs (12288 x 5120, 2048 rows 219 us, 1.18 PFLOP/s; the
+// cycles that the product runs (12288 x 5120, 2048 rows 214 us, 1.20 PFLOP/s; the
 // library's bf16 product 241).  Experts: 16 x 3200 x 5120, 8192 rows of codes 161 us:
 // 936 workgroups, two rounds of the 512 that run at once, where 1.8 would do.
 #include "spense_experts_device.h"
