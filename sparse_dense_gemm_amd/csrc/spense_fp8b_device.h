@@ -120,13 +120,16 @@ __device__ __forceinline__ void load_row8(const XT* x, int64_t k, int64_t K, flo
     }
     return;
   }
+  // the loads go out together: no branch around one
+  XT u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = x[k + i < K ? k + i : K - 1];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v[i] = 0.f;
-    if (k + i < K) {
-      if constexpr (sizeof(XT) == 2) v[i] = __uint_as_float((uint32_t)x[k + i] << 16);
-      else v[i] = x[k + i];
-    }
+    float f;
+    if constexpr (sizeof(XT) == 2) f = __uint_as_float((uint32_t)u[i] << 16);
+    else f = u[i];
+    v[i] = k + i < K ? f : 0.f;
   }
 }
 

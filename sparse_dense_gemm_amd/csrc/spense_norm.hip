@@ -64,6 +64,14 @@ __device__ __forceinline__ float rms_scale(float s, const spense_norm& n, float 
   return r > 0.f ? better : r;  // x infinite
 }
 
+// The end of a row of H columns.  kWhole: H is a multiple of eight.  kShift: at
+// least eight; the last piece of a row is its last eight columns, of which it
+// leaves out the d that the piece before has (in place those may be stored already
+// when it reads them), so that no lane branches around its loads: 6731 rows of 574
+// columns, each of four fp32 rows, 18.5 us, 29.5 with the last lane's values loaded
+// one by one.  kAny: one by one.
+enum Ends { kWhole, kShift, kAny };
+
 // Eight values of a row as they are stored: loads go out together and are widened
 // where they are used (a widening beside its load is a wait for it).
 template <typename XT>
@@ -71,9 +79,10 @@ struct Raw;
 template <>
 struct Raw<uint16_t> {
   u32x4 a;
-  template <bool WHOLE>
+  template <Ends E>
   __device__ __forceinline__ void load(const uint16_t* x, int64_t k, int64_t H) {
-    if (WHOLE || k + 8 <= H) {
+    if constexpr (E == kShift) k = k + 8 <= H ? k : H - 8;
+    if (E != kAny || k + 8 <= H) {
       a = *(const u32x4_any*)(x + k);
     } else {
       a = u32x4{0, 0, 0, 0};
@@ -89,9 +98,10 @@ struct Raw<uint16_t> {
 template <>
 struct Raw<float> {
   f32x4 a, b;
-  template <bool WHOLE>
+  template <Ends E>
   __device__ __forceinline__ void load(const float* x, int64_t k, int64_t H) {
-    if (WHOLE || k + 8 <= H) {
+    if constexpr (E == kShift) k = k + 8 <= H ? k : H - 8;
+    if (E != kAny || k + 8 <= H) {
       a = *(const f32x4_any*)(x + k);
       b = *(const f32x4_any*)(x + k + 4);
     } else {
@@ -107,10 +117,10 @@ struct Raw<float> {
 struct RawAny {
   Raw<float> f;
   Raw<uint16_t> h;
-  template <bool WHOLE>
+  template <Ends E>
   __device__ __forceinline__ void load(const void* p, bool f32, int64_t row, int64_t k, int64_t H) {
-    if (f32) f.load<WHOLE>((const float*)p + row, k, H);
-    else h.load<WHOLE>((const uint16_t*)p + row, k, H);
+    if (f32) f.load<E>((const float*)p + row, k, H);
+    else h.load<E>((const uint16_t*)p + row, k, H);
   }
   __device__ __forceinline__ void multiply(bool f32, float (&v)[8]) const {
     if (f32) {
@@ -123,9 +133,10 @@ struct RawAny {
   }
 };
 
-// Columns k .. k + 7 of a row's operands.  OT, RT: types of O and of the residual;
-// POS: O's rows are summed over j.  Columns from H on are zeros.
-template <typename OT, typename RT, bool POS, bool WHOLE>
+// Columns k .. k + 7 of a row's operands (kShift: at the row's end H - 8 .. H - 1).
+// OT, RT: types of O and of the residual; POS: O's rows are summed over j.  Columns
+// from H on are zeros.
+template <typename OT, typename RT, bool POS, Ends E>
 struct Piece {
   Raw<OT> o[POS ? 2 : 1];
   Raw<RT> res;
@@ -134,8 +145,8 @@ struct Piece {
 
   __device__ __forceinline__ void load_row(const spense_norm& n, int64_t t, int64_t k) {
     if constexpr (POS) load_two(n, t, k, 0);
-    else o[0].template load<WHOLE>((const OT*)n.O + t * n.ldo, k, n.H);
-    if (n.residual) res.template load<WHOLE>((const RT*)n.residual + t * n.ldr, k, n.H);
+    else o[0].template load<E>((const OT*)n.O + t * n.ldo, k, n.H);
+    if (n.residual) res.template load<E>((const RT*)n.residual + t * n.ldr, k, n.H);
   }
   // rows j0 and j0 + 1 of the sum over j
   __device__ __forceinline__ void load_two(const spense_norm& n, int64_t t, int64_t k, int j0) {
@@ -146,15 +157,15 @@ struct Piece {
       const int64_t at = n.pos[t * n.k + j0 + j];
       if (at < 0 || at >= n.O_rows) continue;
       w[j] = n.weights[t * n.k + j0 + j];
-      o[j].template load<WHOLE>((const OT*)n.O + at * n.ldo, k, n.H);
+      o[j].template load<E>((const OT*)n.O + at * n.ldo, k, n.H);
     }
   }
   __device__ __forceinline__ void load_gate(const spense_norm& n, int64_t t, int64_t k) {
-    if (n.post) post.load<WHOLE>(n.post, n.wtype == DT_F32, 0, k, n.H);
-    if (n.gate) gate.load<WHOLE>(n.gate, n.gtype == DT_F32, t * n.ldg, k, n.H);
+    if (n.post) post.load<E>(n.post, n.wtype == DT_F32, 0, k, n.H);
+    if (n.gate) gate.load<E>(n.gate, n.gtype == DT_F32, t * n.ldg, k, n.H);
   }
   __device__ __forceinline__ void load_pre(const spense_norm& n, int64_t k) {
-    if (n.Y && n.pre) pre.load<WHOLE>(n.pre, n.wtype == DT_F32, 0, k, n.H);
+    if (n.Y && n.pre) pre.load<E>(n.pre, n.wtype == DT_F32, 0, k, n.H);
   }
 
   __device__ __forceinline__ void get_o(const spense_norm& n, int64_t t, int64_t k, float (&v)[8]) {
@@ -198,23 +209,48 @@ struct Piece {
   }
 };
 
-template <bool WHOLE, bool STREAM, typename YT>
-__device__ __forceinline__ void put8(const spense_norm& n, YT* y, int64_t k, const float (&v)[8]) {
-  store_row8<STREAM>(y, k, WHOLE ? k + 8 : n.H, v);
+// Values that the piece before has, left out of sums and of a block's maximum.
+template <Ends E>
+__device__ __forceinline__ void drop(float (&v)[8], int d) {
+  if (E == kShift && d > 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) v[i] = i < d ? 0.f : v[i];
+  }
+}
+
+template <Ends E, bool STREAM, typename YT>
+__device__ __forceinline__ void put8(const spense_norm& n, YT* y, int64_t k, int d, const float (&v)[8]) {
+  if (E == kShift && d > 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i >= d) {
+        if constexpr (sizeof(YT) == 2) y[k - d + i] = (YT)bf16_rne(v[i]);
+        else y[k - d + i] = v[i];
+      }
+  } else {
+    store_row8<STREAM>(y, k, E == kAny ? n.H : k + 8, v);
+  }
 }
 
 // y out, of all sixteen lanes that share a block (in: columns below H)
-template <bool WHOLE, bool STREAM>
-__device__ __forceinline__ void put_y(const spense_norm& n, int64_t t, int64_t k, bool in, const float (&y)[8]) {
+template <Ends E, bool STREAM>
+__device__ __forceinline__ void put_y(const spense_norm& n, int64_t t, int64_t k, int d, bool in, const float (&y)[8]) {
   if (n.ytype == DT_FP8) {
     const float s = block_scale(row_max(in ? top8(y) : 0u));
     if (!in) return;
     uint8_t* out = (uint8_t*)n.Y + t * n.ldy;
-    store_codes8<STREAM>(out, k, WHOLE ? k + 8 : n.H, codes8(y, s));
+    const u32x2 c = codes8(y, s);
+    if (E == kShift && d > 0) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i >= d) out[k - d + i] = (uint8_t)(c[i >> 2] >> (8 * (i & 3)));
+    } else {
+      store_codes8<STREAM>(out, k, E == kAny ? n.H : k + 8, c);
+    }
     if (k % kFp8Block == 0) n.yscales[t * n.lds + k / kFp8Block] = s;
   } else if (in) {
-    if (n.ytype == DT_F32) put8<WHOLE, STREAM>(n, (float*)n.Y + t * n.ldy, k, y);
-    else put8<WHOLE, STREAM>(n, (uint16_t*)n.Y + t * n.ldy, k, y);
+    if (n.ytype == DT_F32) put8<E, STREAM>(n, (float*)n.Y + t * n.ldy, k, d, y);
+    else put8<E, STREAM>(n, (uint16_t*)n.Y + t * n.ldy, k, d, y);
   }
 }
 
@@ -227,20 +263,22 @@ __device__ __forceinline__ float sum_of_squares(const float (&v)[8]) {
 
 // A workgroup takes a row, a thread C pieces of eight columns, in registers
 // between the sums.  Eight columns are one load of bf16.
-template <typename OT, typename RT, bool POS, bool WHOLE, bool STREAM, int C>
+template <typename OT, typename RT, bool POS, Ends E, bool STREAM, int C>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(spense_norm n, float rh) {
   __shared__ float tmp[2][16];
   const int64_t t = blockIdx.x;
   const int64_t step = (int64_t)blockDim.x * 8, k0 = (int64_t)threadIdx.x * 8;
   // several pieces: no registers for the weights and gates, which are loaded where they are used
   constexpr bool kHold = C == 1;
-  Piece<OT, RT, POS, WHOLE> p[C];
+  Piece<OT, RT, POS, E> p[C];
   float v[C][8];
   bool in[C];
+  int d[C];  // columns at the piece's beginning that the one before has
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int64_t k = k0 + c * step;
     in[c] = k < n.H;
+    d[c] = E == kShift && in[c] && k + 8 > n.H ? (int)(k + 8 - n.H) : 0;
     if (in[c]) p[c].load_row(n, t, k);
   }
   if constexpr (kHold) {
@@ -258,7 +296,10 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(spense_norm n, float 
   if (n.post) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (in[c]) s += sum_of_squares(v[c]);
+      if (in[c]) {
+        drop<E>(v[c], d[c]);
+        s += sum_of_squares(v[c]);
+      }
     inv = rms_scale(block_sum(s, tmp[0]), n, rh);
     s = 0.f;
   }
@@ -268,7 +309,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(spense_norm n, float 
       const int64_t k = k0 + c * step;
       if constexpr (!kHold) p[c].load_gate(n, t, k);
       p[c].get_r(n, inv, v[c]);
-      if (n.residual_out) put8<WHOLE, STREAM>(n, (RT*)n.residual_out + t * n.ldro, k, v[c]);
+      if (n.residual_out) put8<E, STREAM>(n, (RT*)n.residual_out + t * n.ldro, k, d[c], v[c]);
+      drop<E>(v[c], d[c]);
       s += sum_of_squares(v[c]);
     }
   if (!n.Y) return;
@@ -279,19 +321,21 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(spense_norm n, float 
     if (in[c]) {
       if constexpr (!kHold) p[c].load_pre(n, k);
       p[c].get_y(n, inv, v[c]);
+      drop<E>(v[c], d[c]);
     }
-    put_y<WHOLE, STREAM>(n, t, k, in[c], v[c]);
+    put_y<E, STREAM>(n, t, k, d[c], in[c], v[c]);
   }
 }
 
-// Rows that do not fit the registers of a workgroup: read again for each sum.
+// Rows that do not fit the registers of a workgroup, read again for each sum, and
+// rows of fewer than eight columns.
 template <typename OT, typename RT, bool POS, bool STREAM>
 __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(spense_norm n, float rh) {
   __shared__ float tmp[2][16];
   const int64_t t = blockIdx.x;
   const int64_t step = (int64_t)blockDim.x * 8, k0 = (int64_t)threadIdx.x * 8;
   float inv = 1.f, inv2 = 1.f, s = 0.f;
-  Piece<OT, RT, POS, false> p;
+  Piece<OT, RT, POS, kAny> p;
   float v[8];
   auto get_r = [&](int64_t k) __attribute__((always_inline)) {
     p.load_row(n, t, k);
@@ -322,14 +366,14 @@ __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(spense_norm n, f
     const bool in = k < n.H;
     if (in) {
       get_r(k);
-      if (n.residual_out) put8<false, STREAM>(n, (RT*)n.residual_out + t * n.ldro, k, v);
+      if (n.residual_out) put8<kAny, STREAM>(n, (RT*)n.residual_out + t * n.ldro, k, 0, v);
     }
     if (!n.Y) continue;
     if (in) {
       p.load_pre(n, k);
       p.get_y(n, inv2, v);
     }
-    put_y<false, STREAM>(n, t, k, in, v);
+    put_y<kAny, STREAM>(n, t, k, 0, in, v);
   }
 }
 
@@ -340,11 +384,13 @@ hipError_t launch(const spense_norm& n, hipStream_t s) {
   const bool whole = n.H % 8 == 0;
   const float rh = 1.0f / (float)n.H;
   auto threads = [&](int64_t c) { return (unsigned)(((pieces + c - 1) / c + 63) / 64 * 64); };
-  if (pieces <= kMaxThreads) {
-    auto k = whole ? norm_kernel<OT, RT, POS, true, STREAM, 1> : norm_kernel<OT, RT, POS, false, STREAM, 1>;
+  if (n.H < 8) {
+    norm_long_kernel<OT, RT, POS, STREAM><<<T, 64, 0, s>>>(n, rh);
+  } else if (pieces <= kMaxThreads) {
+    auto k = whole ? norm_kernel<OT, RT, POS, kWhole, STREAM, 1> : norm_kernel<OT, RT, POS, kShift, STREAM, 1>;
     k<<<T, threads(1), 0, s>>>(n, rh);
   } else if (pieces <= 4 * kMaxThreads) {
-    auto k = whole ? norm_kernel<OT, RT, POS, true, STREAM, 4> : norm_kernel<OT, RT, POS, false, STREAM, 4>;
+    auto k = whole ? norm_kernel<OT, RT, POS, kWhole, STREAM, 4> : norm_kernel<OT, RT, POS, kShift, STREAM, 4>;
     k<<<T, threads(4), 0, s>>>(n, rh);
   } else {
     norm_long_kernel<OT, RT, POS, STREAM><<<T, kMaxThreads, 0, s>>>(n, rh);

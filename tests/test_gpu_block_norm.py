@@ -276,3 +276,34 @@ def test_pointers_of_an_empty_o():
     import ctypes
     assert sdg._lib().spense_block_norm(ctypes.byref(call), torch.cuda.current_stream().cuda_stream) == 0
     assert (Y == 0).all()
+
+
+@pytest.mark.parametrize("H", [9, 10, 11, 13, 15, 63, 65, 121, 127, 130, 135, 517, 575, 8199, 9001])
+@pytest.mark.parametrize("k", [0, 2])
+def test_row_ends(H, k):
+    """Rows that end inside a piece of eight columns, also with the residual in place and unaligned rows."""
+    for y in ("f32", "bf16", "fp8"):
+        d = tensors(5, H, H + k, o="bf16", r="bf16", w="bf16", gate="token", g="bf16", k=k)
+        check(d, "bf16", y, 5, H, (H, k, y), pad=3)
+        R2, Y, ys = run(d, "bf16", y, 5, H)
+        d["residual"] = d["residual"].clone()
+        S2, Z, zs = run(d, "bf16", y, 5, H, inplace=True)
+        assert torch.equal(R2, S2) and torch.equal(Y, Z) and (ys is None or torch.equal(ys, zs))
+
+
+@pytest.mark.parametrize("H,col", [(130, 125), (130, 127), (130, 128), (130, 121), (135, 127), (135, 128), (14, 7), (14, 8)])
+@pytest.mark.parametrize("y", ["f32", "bf16", "fp8"])
+def test_one_column_of_the_last_norm_stays_in_its_place(H, col, y):
+    """A NaN in `pre` reaches its own column alone, or its block of codes."""
+    d = tensors(3, H, 1, w="f32")
+    _, want, wants = run(d, "f32", y, 3, H)
+    d["pre"][col] = float("nan")
+    _, Y, ys = run(d, "f32", y, 3, H)
+    at = torch.arange(H, device="cuda")
+    if y == "fp8":
+        b = col // 128
+        assert ys[:, b].isnan().all() and (Y[:, at // 128 == b] == 0).all()
+        others = torch.arange(ys.shape[1], device="cuda") != b
+        assert torch.equal(ys[:, others], wants[:, others]) and torch.equal(Y[:, at // 128 != b], want[:, at // 128 != b])
+    else:
+        assert Y[:, col].isnan().all() and torch.equal(Y[:, at != col], want[:, at != col])
