@@ -52,13 +52,14 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(const XT* X, int64
   constexpr int kPer = kFp8Block * kLanes / 256;  // rows of a thread, 16 apart
   float v[kPer][8];
   uint32_t m = 0;
+  // past the last row that row again, which changes no maximum: all rows' loads go
+  // out together
+  auto load = [&](int64_t end) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int64_t r = r0 + 16 * i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (r < M) load_row8<XT>(X + r * ldx, k, K, v[i]);
-  }
+    for (int i = 0; i < kPer; ++i) load_row8<XT>(X + (r0 + 16 * i < M ? r0 + 16 * i : M - 1) * ldx, k, end, v[i]);
+  };
+  if (k + 8 <= K) load(k + 8);
+  else load(K);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const uint32_t t = top8(v[i]);
@@ -97,9 +98,11 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, i
   if (k + 8 <= K) {
     c = *(const u32x2_any*)in;
   } else {
+    uint8_t u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (k + i < K) c[i >> 2] |= (uint32_t)in[i] << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) u[i] = in[k + i < K ? i : 0];  // no branch around a load
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i >> 2] |= (k + i < K ? (uint32_t)u[i] : 0u) << (8 * (i & 3));
   }
   const float s = scales[row / rows * lds + k / kFp8Block];
   float v[8];
