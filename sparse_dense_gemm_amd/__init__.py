@@ -662,7 +662,8 @@ def spense_pack_fp8b(codes, scales, *, N: Optional[int] = None, K: Optional[int]
 
 
 def spense_linear_fp8b(h: int, codes, scales, Y, *, M: Optional[int] = None, stream=None) -> None:
-    """Y = X . W^T on an fp8b layer, X the codes (bytes [M, K]) and scales (float32 [M, ceil(K / 128)])."""
+    """Y = X . W^T on an fp8b layer, X the codes (bytes [M, K]) and scales (float32 [M, ceil(K / 128)]).  float32 Y: sums
+    in full; bfloat16 Y: sums of eight products at a time that keep 13 bits below the largest of them."""
     _linear_fp8b(h, _dims(h), codes, scales, Y, M, stream)
 
 
@@ -696,7 +697,8 @@ def spense_pack_experts_fp8b(W, scales, *, K: Optional[int] = None, glu: bool = 
 
 def spense_experts_linear_fp8b(h: int, codes, scales, offsets, Y, *, rows=None, R: Optional[int] = None,
                                stream=None) -> None:
-    """spense_experts_linear on quantised activations: codes (bytes [M, K]) and scales (float32 [M, ceil(K / 128)])."""
+    """spense_experts_linear on quantised activations: codes (bytes [M, K]) and scales (float32 [M, ceil(K / 128)]).  Bits
+    of the sums by Y's type, as spense_linear_fp8b."""
     _experts_linear_fp8b(h, _dims(h), codes, scales, offsets, Y, rows, R, stream)
 
 
@@ -887,7 +889,8 @@ class SpenseExperts(_Owned):
 
 class SpenseLinearFp8b(_Owned):
     """Owns one packed fp8b layer; ``layer(X, Y)`` runs spense_linear, ``layer.w8a8(X, Y)`` spense_linear_w8a8,
-    ``layer.quantized(codes, scales, Y)`` spense_linear_fp8b."""
+    ``layer.quantized(codes, scales, Y)`` spense_linear_fp8b.  The last two keep fewer bits of the sums for a bfloat16 Y
+    (spense_linear_fp8b)."""
 
     def __init__(self, codes, scales, **kw):
         self.handle = spense_pack_fp8b(codes, scales, **kw)

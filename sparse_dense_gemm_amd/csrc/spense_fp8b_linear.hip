@@ -16,7 +16,8 @@
 //           13 bits below the largest of them (a product of 2^2 beside one of 2^16;
 //           measured, and the same of 16x16x32 and with any operand as the eight);
 //           on normal inputs that is 2e-5 of the result, a hundredth of the rounding
-//           to bf16, for 3.5 times the rate of the 16x16x32 products;
+//           to bf16, for 3.5 times the rate of the 16x16x32 products (where large
+//           products cancel it is more than that rounding: such callers take fp32);
 //   kWide   codes x, Y in fp32: both widened to bf16, whose products and sums keep
 //           the bits (6e-8 of the result).
 // The scales cost four vector instructions to each 16x16x128, which takes the time
