@@ -14,6 +14,7 @@
 // at 4.7 TB/s; 2048 rows of 5120, each the sum of two fp32 rows, 28 us, 147 MB at 5.3.
 // One row takes 3.0 us, most of it the launch and the wait for its loads.
 #include <algorithm>
+#include <cfloat>
 
 #include "spense_fp8b_device.h"
 
@@ -51,12 +52,14 @@ __device__ __forceinline__ float block_sum(float v, float* tmp) {
   return row_sum(i < waves ? tmp[i] : 0.f);
 }
 
-// 1 / sqrt(s / H + eps), rh = 1 / H.  The root instruction is off by up to a unit in
-// the last place, which one step takes to little more than half of one (t + d is
-// x r exactly); eps is a normal number, so x is.  It costs ten instructions a row,
-// and halves the codes that differ from those of the exact norm.
+// 1 / sqrt(s / H + eps), rh = 1 / H.  Every finite sum is divided; an infinite one
+// gives 0, as in the formula, and a NaN a NaN.  The root instruction is off by up to
+// a unit in the last place, which one step takes to little more than half of one
+// (t + d is x r exactly); eps is a normal number, so x is.  It costs ten
+// instructions a row.  A block of codes does not see the second norm's factor, up to
+// roundings: its scale takes that up.
 __device__ __forceinline__ float rms_scale(float s, const spense_norm& n, float rh) {
-  const float x = (s < 3.0e38f ? quotient(s, (float)n.H, rh) : s) + n.eps;  // an infinite sum: 0, as in the formula
+  const float x = (s <= FLT_MAX ? quotient(s, (float)n.H, rh) : s) + n.eps;
   const float r = __builtin_amdgcn_rsqf(x);
   const float t = x * r, d = fmaf(x, r, -t);
   const float e = fmaf(-d, r, fmaf(-t, r, 1.0f));
