@@ -5,6 +5,7 @@
 
 #include "spense_device.h"
 #include "spense_fp8b.h"
+#include "spense_quotient.h"
 
 namespace spense {
 namespace {
@@ -26,17 +27,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// The quotient x / d rounded to 32 bits, r = 1 / d within a unit in the last
-// place: two steps q += r (x - q d) in fused multiply-adds.  The first leaves q
-// within a unit in the last place, the second's remainder is exact, and its sum
-// rounds as the division does.  Five instructions where the division takes ten;
-// it needs d, r and the remainders in the normal range.
-__device__ __forceinline__ float quotient(float x, float d, float r) {
-  float q = x * r;
-  q = fmaf(fmaf(-q, d, x), r, q);
-  return fmaf(fmaf(-q, d, x), r, q);
-}
-
 // The scale of a block whose largest magnitude has the fp32 bits `m`: the
 // quotient by 448, 1 where that is 0, NaN for a block that holds a NaN or an
 // infinity.
@@ -51,12 +41,11 @@ __device__ __forceinline__ float block_scale(uint32_t m) {
 // The codes of four values of a block: e4m3(x / s), x / s being the 32-bit
 // quotient (2048 x 27648 bf16 is bound by memory also with a division, but its
 // vector instructions then take 29 instead of 17 us of 34).  Scales outside
-// [2^-90, 2^100] divide.
+// [2^-90, 2^100], and those whose significand is all ones, divide.
 __device__ __forceinline__ uint32_t codes4(const f32x4& x, float s) {
   f32x4 q;
-  if (s >= 0x1p-90f && s <= 0x1p100f) {
-    float r = __builtin_amdgcn_rcpf(s);
-    r = fmaf(fmaf(-s, r, 1.0f), r, r);
+  if (by_reciprocal(s, __float_as_uint(s))) {
+    const float r = reciprocal(s, __builtin_amdgcn_rcpf(s));
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = __builtin_copysignf(quotient(x[i], s, r), x[i]);  // -0 stays
   } else {
