@@ -354,9 +354,15 @@ int spense_block_norm(const spense_norm* n, void* stream) {
     return SPENSE_EINVAL;
   if (n->residual && n->residual == n->residual_out && n->ldr != n->ldro) return SPENSE_EINVAL;
   if (n->T > 0) {  // a row is read by several sums, and picked rows by several workgroups
-    for (const void* in : {n->O, n->post, n->pre, n->gate})
-      if (in && (in == n->residual_out || in == n->Y)) return SPENSE_EINVAL;
-    if (n->Y && (n->Y == n->residual || n->Y == n->residual_out)) return SPENSE_EINVAL;
+    const void* const outs[] = {n->residual_out, n->Y, n->yscales};
+    for (int i = 0; i < 3; ++i) {
+      if (!outs[i]) continue;
+      for (const void* in : {n->O, (const void*)n->pos, (const void*)n->weights, n->post, n->pre, n->gate})
+        if (outs[i] == in) return SPENSE_EINVAL;
+      if (i > 0 && outs[i] == n->residual) return SPENSE_EINVAL;  // the sum itself may take its place
+      for (int j = 0; j < i; ++j)
+        if (outs[i] == outs[j]) return SPENSE_EINVAL;
+    }
   }
   const struct {
     bool used;
