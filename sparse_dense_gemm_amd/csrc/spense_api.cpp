@@ -782,7 +782,10 @@ static int grow_workspaces(spense_layer* h, const WsNeed& need, hipStream_t s) {
     h->n_counters = bytes / 4;
     if (rc == SPENSE_OK) {
       e = launch_zero_i32(h->counters, (int64_t)need.cnt, s);
-      if (e != hipSuccess) rc = hip_fail(e);
+      if (e != hipSuccess) {  // they hold anything: no later call may take them as zeros
+        rc = hip_fail(e);
+        h->n_counters = 0;
+      }
     }
   }
   return rc;

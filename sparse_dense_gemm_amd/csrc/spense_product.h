@@ -147,7 +147,10 @@ struct ProductWorkspaces {
       n_counters = bytes / 4;
       if (rc == SPENSE_OK) {
         e = launch_zero_i32(counters, n.cnt, s);
-        if (e != hipSuccess) rc = status_of(e);
+        if (e != hipSuccess) {  // they hold anything: no later call may take them as zeros
+          rc = status_of(e);
+          n_counters = 0;
+        }
       }
     }
     return rc;
