@@ -759,35 +759,34 @@ static WsNeed large_batch_bound(const LayerDesc& d) {
 
 // Replaces h's workspaces with ones of at least `need` (synchronising the
 // stream first: earlier launches may still use the old ones; those that a graph
-// may hold stay).  New counters are cleared by a fill kernel on the stream.
+// may hold stay).  New counters are cleared by a fill kernel on the stream.  One
+// that cannot be replaced stays as it is.
 static int grow_workspaces(spense_layer* h, const WsNeed& need, hipStream_t s) {
   if (need.fits(h)) return SPENSE_OK;
   hipError_t e = hipStreamSynchronize(s);
   if (e != hipSuccess) return hip_fail(e);
-  auto regrow = [&](int which, void** ptr, size_t& have, size_t want) -> int {
+  auto regrow = [&](int which, void** ptr, size_t& have, size_t want, auto&& fill) -> int {
     if (want <= have) return SPENSE_OK;
-    if (!h->graphs.drop(which, *ptr)) return SPENSE_ENOMEM;
-    *ptr = nullptr;
-    have = 0;
-    const hipError_t err = hipMalloc(ptr, want);
+    void* fresh = nullptr;
+    hipError_t err = hipMalloc(&fresh, want);
     if (err != hipSuccess) return err == hipErrorOutOfMemory ? (g_last_hip = (int)err, SPENSE_ENOMEM) : hip_fail(err);
+    err = fill(fresh);
+    if (err != hipSuccess || !h->graphs.drop(which, *ptr)) {
+      (void)hipFree(fresh);
+      return err == hipSuccess ? SPENSE_ENOMEM : hip_fail(err);
+    }
+    *ptr = fresh;
     have = want;
     return SPENSE_OK;
   };
-  int rc = regrow(kWsX, &h->xws, h->xws_bytes, need.xws);
-  if (rc == SPENSE_OK) rc = regrow(kWsPartials, (void**)&h->ws, h->ws_bytes, need.ws);
-  if (rc == SPENSE_OK && need.cnt > h->n_counters) {
-    size_t bytes = h->n_counters * 4;
-    rc = regrow(kWsCounters, (void**)&h->counters, bytes, need.cnt * 4);
-    h->n_counters = bytes / 4;
-    if (rc == SPENSE_OK) {
-      e = launch_zero_i32(h->counters, (int64_t)need.cnt, s);
-      if (e != hipSuccess) {  // they hold anything: no later call may take them as zeros
-        rc = hip_fail(e);
-        h->n_counters = 0;
-      }
-    }
-  }
+  auto as_is = [](void*) { return hipSuccess; };
+  int rc = regrow(kWsX, &h->xws, h->xws_bytes, need.xws, as_is);
+  if (rc == SPENSE_OK) rc = regrow(kWsPartials, (void**)&h->ws, h->ws_bytes, need.ws, as_is);
+  size_t bytes = h->n_counters * 4;
+  if (rc == SPENSE_OK)
+    rc = regrow(kWsCounters, (void**)&h->counters, bytes, need.cnt * 4,
+                [&](void* p) { return launch_zero_i32((int32_t*)p, (int64_t)need.cnt, s); });
+  h->n_counters = bytes / 4;
   return rc;
 }
 

@@ -126,33 +126,32 @@ struct ProductWorkspaces {
 
   // Replaces the workspaces that are too small (earlier launches may still use
   // them, so the stream is synchronised first; those that a graph may hold stay).
+  // One that cannot be replaced stays as it is, and so does what it suffices for.
   int grow(const Need& n, hipStream_t s) {
     hipError_t e = hipStreamSynchronize(s);
     if (e != hipSuccess) return status_of(e);
-    auto regrow = [&](int which, void** p, size_t& have, int64_t want) -> int {
+    auto regrow = [&](int which, void** p, size_t& have, int64_t want, auto&& fill) -> int {
       if (want <= (int64_t)have) return SPENSE_OK;
-      if (!graphs.drop(which, *p)) return SPENSE_ENOMEM;
-      *p = nullptr;
-      have = 0;
-      const hipError_t err = hipMalloc(p, (size_t)want);
+      void* fresh = nullptr;
+      hipError_t err = hipMalloc(&fresh, (size_t)want);
       if (err != hipSuccess) return status_of(err);
+      err = fill(fresh);
+      if (err != hipSuccess || !graphs.drop(which, *p)) {
+        (void)hipFree(fresh);
+        return err == hipSuccess ? SPENSE_ENOMEM : status_of(err);
+      }
+      *p = fresh;
       have = (size_t)want;
       return SPENSE_OK;
     };
-    int rc = regrow(kWsX, (void**)&xws, xws_bytes, n.xws);
-    if (rc == SPENSE_OK) rc = regrow(kWsPartials, (void**)&ws, ws_bytes, n.ws);
-    if (rc == SPENSE_OK && n.cnt > (int64_t)n_counters) {
-      size_t bytes = n_counters * 4;
-      rc = regrow(kWsCounters, (void**)&counters, bytes, n.cnt * 4);
-      n_counters = bytes / 4;
-      if (rc == SPENSE_OK) {
-        e = launch_zero_i32(counters, n.cnt, s);
-        if (e != hipSuccess) {  // they hold anything: no later call may take them as zeros
-          rc = status_of(e);
-          n_counters = 0;
-        }
-      }
-    }
+    auto as_is = [](void*) { return hipSuccess; };
+    int rc = regrow(kWsX, (void**)&xws, xws_bytes, n.xws, as_is);
+    if (rc == SPENSE_OK) rc = regrow(kWsPartials, (void**)&ws, ws_bytes, n.ws, as_is);
+    size_t bytes = n_counters * 4;
+    if (rc == SPENSE_OK)
+      rc = regrow(kWsCounters, (void**)&counters, bytes, n.cnt * 4,
+                  [&](void* p) { return launch_zero_i32((int32_t*)p, n.cnt, s); });
+    n_counters = bytes / 4;
     return rc;
   }
 };

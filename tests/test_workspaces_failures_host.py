@@ -114,3 +114,31 @@ def test_counters_are_zeroed_before_they_are_used(lib, kind):
     assert counters(lib) and counters(lib) == lib.host_zeroed()
     lib.spense_free(h)
     assert lib.host_live_bytes() == 0
+
+
+@pytest.mark.parametrize("kind", CALLS)
+@pytest.mark.parametrize("bytes_", [1, 1 << 12, 1 << 16], ids=["any", "4K", "64K"])
+def test_a_failed_call_takes_nothing_from_the_others(lib, kind, bytes_):
+    """What could be captured before a call that could not grow the workspaces still can after it."""
+    make, run = CALLS[kind]
+
+    def capturable(sizes):
+        lib.host_capturing(1)
+        good = [M for M in sizes if run(lib, h, M) == 0]
+        lib.host_capturing(0)
+        return good
+
+    for first, larger in ((64, 700), (700, 5000), (3000, 8000), (9000, 20000)):
+        h = pack(lib, make)
+        assert run(lib, h, first) == 0
+        sizes = range(1, first + 1, 1 + first // 200)
+        before = capturable(sizes)
+        assert before
+        held = lib.host_live_bytes()
+        lib.host_fail_alloc(bytes_)
+        failed = run(lib, h, larger) != 0  # where it needs an allocation of that size
+        lib.host_fail_alloc(0)
+        assert capturable(sizes) == before, (kind, first, larger)
+        assert not failed or lib.host_live_bytes() >= held
+        lib.spense_free(h)
+    assert lib.host_live_bytes() == 0
