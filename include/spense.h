@@ -691,7 +691,8 @@ int spense_free(spense_handle h);
 /* Human-readable text for a status code (static storage). */
 const char* spense_strerror(int status);
 
-/* hipError_t value of the most recent SPENSE_EHIP on the calling thread (0 if none). */
+/* hipError_t value of the most recent SPENSE_EHIP or SPENSE_ENOMEM on the calling thread (0 if none); the runtime's own
+ * last error has been taken. */
 int spense_last_hip_error(void);
 
 /* SPENSE_ABI_VERSION of the loaded library. */

@@ -23,9 +23,17 @@ namespace {
 
 thread_local int g_last_hip = 0;
 
+// The runtime keeps an error until it is asked for: taken here, so that the next
+// launch of this thread, the library's or another's, does not report it.
 int hip_fail(hipError_t e) {
   g_last_hip = (int)e;
+  (void)hipGetLastError();
   return SPENSE_EHIP;
+}
+
+int alloc_fail(hipError_t e) {
+  const int rc = hip_fail(e);
+  return e == hipErrorOutOfMemory ? SPENSE_ENOMEM : rc;
 }
 
 bool valid_dtype(int32_t t) { return t == SPENSE_F32 || t == SPENSE_BF16 || t == SPENSE_FP8_E4M3; }
@@ -210,7 +218,7 @@ int build_layer(const void* W, int32_t wdtype, int64_t N, int64_t K, int64_t ldw
   if (e != hipSuccess) {
     (void)hipStreamSynchronize(s);
     release(h);
-    return e == hipErrorOutOfMemory ? (g_last_hip = (int)e, SPENSE_ENOMEM) : hip_fail(e);
+    return alloc_fail(e);
   }
   *out = h;
   return SPENSE_OK;
@@ -769,7 +777,7 @@ static int grow_workspaces(spense_layer* h, const WsNeed& need, hipStream_t s) {
     if (want <= have) return SPENSE_OK;
     void* fresh = nullptr;
     hipError_t err = hipMalloc(&fresh, want);
-    if (err != hipSuccess) return err == hipErrorOutOfMemory ? (g_last_hip = (int)err, SPENSE_ENOMEM) : hip_fail(err);
+    if (err != hipSuccess) return alloc_fail(err);
     err = fill(fresh);
     if (err != hipSuccess || !h->graphs.drop(which, *ptr)) {
       (void)hipFree(fresh);
@@ -1174,7 +1182,7 @@ int spense_score_glu(const void* W_gu, const void* W_down, int32_t wdtype, int64
   const size_t n_floats = (size_t)(H + I + nchunks * std::max(H, I) + 2 * I + I);
   float* tmp = nullptr;
   hipError_t e = hipMalloc((void**)&tmp, n_floats * 4);
-  if (e != hipSuccess) return e == hipErrorOutOfMemory ? SPENSE_ENOMEM : hip_fail(e);
+  if (e != hipSuccess) return alloc_fail(e);
   float* hx = tmp;
   float* ha = hx + H;
   float* partial = ha + I;
@@ -1197,7 +1205,7 @@ int spense_select_dense(const float* score, int64_t n, int64_t k, int32_t* dense
   uint8_t* sel = nullptr;  // [n] selection mask, then [n] int32 ranks (4-byte aligned)
   const size_t off = ((size_t)n + 255) / 256 * 256;
   hipError_t e = hipMalloc((void**)&sel, off + (size_t)n * 4);
-  if (e != hipSuccess) return e == hipErrorOutOfMemory ? SPENSE_ENOMEM : hip_fail(e);
+  if (e != hipSuccess) return alloc_fail(e);
   std::vector<uint8_t> h_sel((size_t)n);
   e = launch_rank_select(score, n, k, (int*)(sel + off), sel, s);
   if (e == hipSuccess) e = hipMemcpyAsync(h_sel.data(), sel, (size_t)n, hipMemcpyDeviceToHost, s);

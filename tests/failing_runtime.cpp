@@ -7,6 +7,7 @@ namespace {
 int zero_fails = 0;       // zeroing launches that fail from now on
 int64_t zeroed = 0;       // address that was zeroed last
 int64_t alloc_fails = 0;  // allocations of this many bytes or more fail, once
+hipError_t last = hipSuccess;  // kept until it is asked for, as the runtime does
 }  // namespace
 
 extern "C" {
@@ -15,11 +16,18 @@ void host_fail_zero(int n) { zero_fails = n; }
 int64_t host_zeroed(void) { return zeroed; }
 void host_fail_alloc(int64_t bytes) { alloc_fails = bytes; }
 
+int host_last_error(void) { return (int)last; }
+hipError_t __wrap_hipGetLastError(void) {
+  const hipError_t e = last;
+  last = hipSuccess;
+  return e;
+}
+
 hipError_t __real_hipMalloc(void** p, size_t bytes);
 hipError_t __wrap_hipMalloc(void** p, size_t bytes) {
   if (alloc_fails && (int64_t)bytes >= alloc_fails) {
     alloc_fails = 0;
-    return hipErrorOutOfMemory;
+    return last = hipErrorOutOfMemory;
   }
   return __real_hipMalloc(p, bytes);
 }
@@ -28,7 +36,7 @@ hipError_t __wrap_hipMalloc(void** p, size_t bytes) {
 hipError_t __wrap__ZN6spense15launch_zero_i32EPilP12ihipStream_t(int32_t* p, int64_t, hipStream_t) {
   if (zero_fails > 0) {
     --zero_fails;
-    return hipErrorLaunchFailure;
+    return last = hipErrorLaunchFailure;
   }
   zeroed = (int64_t)p;
   return hipSuccess;

@@ -27,7 +27,7 @@ def lib(tmp_path_factory):
     out = os.path.join(str(tmp_path_factory.mktemp("failing")), "libspense_failing.so")
     src = [os.path.join(hl.CSRC, f) for f in ("spense_api.cpp", "spense_mx_api.cpp", "spense_fp8b_api.cpp")]
     src += [os.path.join(hl.HERE, f) for f in ("host_runtime.cpp", "fp8b_host_runtime.cpp", "failing_runtime.cpp")]
-    r = subprocess.run([gxx, "-std=c++17", "-O1", "-w", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-Wl,--wrap=hipMalloc",
+    r = subprocess.run([gxx, "-std=c++17", "-O1", "-w", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-Wl,--wrap=hipMalloc", "-Wl,--wrap=hipGetLastError",
                         f"-Wl,--wrap={ZERO}", "-D__HIP_PLATFORM_AMD__", f"-I{hl.ROCM}/include", *src, "-o", out],
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
@@ -141,4 +141,24 @@ def test_a_failed_call_takes_nothing_from_the_others(lib, kind, bytes_):
         assert capturable(sizes) == before, (kind, first, larger)
         assert not failed or lib.host_live_bytes() >= held
         lib.spense_free(h)
+    assert lib.host_live_bytes() == 0
+
+
+@pytest.mark.parametrize("kind", CALLS)
+def test_errors_are_taken_from_the_runtime(lib, kind):
+    """A failure is reported once: no later launch of the thread finds it."""
+    make, run = CALLS[kind]
+    h = ctypes.c_void_p()
+    lib.host_fail_alloc(1)
+    assert make(lib, h) == sdg.SPENSE_ENOMEM and not h.value
+    assert lib.host_last_error() == 0
+    h = pack(lib, make)
+    lib.host_fail_alloc(1)
+    assert run(lib, h, 4) == sdg.SPENSE_ENOMEM
+    assert lib.host_last_error() == 0
+    lib.host_fail_zero(1)
+    assert run(lib, h, 4) == sdg.SPENSE_EHIP
+    assert lib.host_last_error() == 0 and lib.spense_last_hip_error() != 0
+    assert run(lib, h, 4) == 0
+    lib.spense_free(h)
     assert lib.host_live_bytes() == 0
