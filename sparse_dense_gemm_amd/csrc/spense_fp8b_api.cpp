@@ -36,10 +36,14 @@ constexpr int64_t kKept = int64_t(96) << 20;
 // and streamed, layers in turn: 131 MB at one row 27.2 and 23.4, at 29 rows 32.9 and
 // 29.0, at 64 rows 35.9 and 33.5; 262 MB of 16 experts, 128 rows 56.5 and 48.4, but
 // 512 rows (two m-groups to some) 76 and 92; 66 MB at one row 14.0 and 15.5.
-bool stream_weights(const Fp8bDesc& d, bool grouped, int64_t R, const ExpertsShape& c) {
-  const int64_t hit = grouped ? std::min(d.E, R) : 1;
+// R16: rows, rounded up to sixteen as the plan has them, so that a launch is the one
+// that its plan priced.  Of few experts' rows less may be read than that counts: us
+// of three layers of 16 experts, 262 MB each, in turn, one row 17.2 and 17.4, two
+// 18.2 and 18.5, five 20.0 and 19.5, ten 23.5 and 22.3.
+bool stream_weights(const Fp8bDesc& d, bool grouped, int64_t R16, const ExpertsShape& c) {
+  const int64_t hit = grouped ? std::min(d.E, R16) : 1;
   if (c.t >= 8 || hit * d.NT * d.tile_bytes <= kKept) return false;
-  return grouped && d.E > 1 ? R <= 8 * c.t * hit : R <= 16 * c.t;
+  return grouped && d.E > 1 ? R16 <= 8 * c.t * hit : R16 <= 16 * c.t;
 }
 
 // Estimated time of a launch of `groups` m-groups, in cycles or so.  Per stage (256
@@ -159,7 +163,7 @@ struct Fp8bLayer final : GroupedLayer {
     a.ldy = ldy;
     a.ydtype = ydtype;
     a.kind = kind;
-    a.stream = stream_weights(d, grouped, R, fp8b_shape(kind, p.config));
+    a.stream = stream_weights(d, grouped, (R + 15) / 16 * 16, fp8b_shape(kind, p.config));
     // The product kernel reads rows of 16-byte pieces through offsets of 31
     // bits: activations are quantised into that form, or read in place if they
     // have it and laid out first if not: the R rows that are read, gathered if
