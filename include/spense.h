@@ -28,6 +28,7 @@
  *   - A size may be zero where its range says so; matrices and lists without
  *     elements may then be NULL.
  *   - Matrices are row-major; leading dimensions are in elements.
+ *   - An output may overlap no operand and no other output, unless a call says so.
  *   - A HIP runtime failure returns SPENSE_EHIP; spense_last_hip_error()
  *     then returns the hipError_t value.  Faults inside a kernel surface at the
  *     caller's next synchronisation, as for any HIP launch.
@@ -512,7 +513,8 @@ int spense_experts_combine(const void* O, int32_t otype, int64_t R, int64_t ldo,
  *
  *   X       device pointer, [M, ldx] of xdtype (SPENSE_F32 or SPENSE_BF16), ldx >= K.
  *   rows    1 or 128.
- * 0 <= M <= 2^24, 1 <= K <= 2^20.  Asynchronous on `stream`.
+ * 0 <= M <= 2^24, 1 <= K <= 2^20.  X, codes and scales may not overlap
+ * (SPENSE_EINVAL where two start at the same address).  Asynchronous on `stream`.
  */
 int spense_quantize_fp8b(const void* X, int32_t xdtype, int64_t M, int64_t K, int64_t ldx, int32_t rows,
                          uint8_t* codes, int64_t ldc, float* scales, int64_t lds, void* stream);
@@ -521,7 +523,8 @@ int spense_quantize_fp8b(const void* X, int32_t xdtype, int64_t M, int64_t K, in
  * spense_dequantize_fp8b - the numbers an fp8b matrix stands for, into Y [M, ldy]
  * of ydtype (SPENSE_F32 or SPENSE_BF16): the product of code and scale, rounded
  * to fp32 and then, for SPENSE_BF16, to bf16.  Sizes as for
- * spense_quantize_fp8b.  Asynchronous on `stream`.
+ * spense_quantize_fp8b; Y may overlap neither codes nor scales (SPENSE_EINVAL where it
+ * starts at their address).  Asynchronous on `stream`.
  */
 int spense_dequantize_fp8b(const uint8_t* codes, int64_t ldc, const float* scales, int64_t lds, int32_t rows,
                            int64_t M, int64_t K, void* Y, int32_t ydtype, int64_t ldy, void* stream);

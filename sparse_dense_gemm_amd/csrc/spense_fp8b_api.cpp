@@ -296,6 +296,9 @@ int spense_quantize_fp8b(const void* X, int32_t xdtype, int64_t M, int64_t K, in
   if (M > 0 && (!X || !codes || !scales)) return SPENSE_EINVAL;
   if (float_status(xdtype) != SPENSE_OK) return float_status(xdtype);
   if (M == 0) return SPENSE_OK;
+  // a row is read by several workgroups
+  if (X == (const void*)codes || X == (const void*)scales || (const void*)codes == (const void*)scales)
+    return SPENSE_EINVAL;
   const hipError_t e = launch_fp8b_quantize(X, xdtype, M, K, ldx, rows, codes, ldc, scales, lds, (hipStream_t)stream);
   return e == hipSuccess ? SPENSE_OK : report_hip(e);
 }
@@ -306,6 +309,7 @@ int spense_dequantize_fp8b(const uint8_t* codes, int64_t ldc, const float* scale
   if (M > 0 && (!codes || !scales || !Y)) return SPENSE_EINVAL;
   if (float_status(ydtype) != SPENSE_OK) return float_status(ydtype);
   if (M == 0) return SPENSE_OK;
+  if (Y == (const void*)codes || Y == (const void*)scales) return SPENSE_EINVAL;
   const hipError_t e = launch_fp8b_dequantize(codes, ldc, scales, lds, rows, M, K, Y, ydtype, ldy, (hipStream_t)stream);
   return e == hipSuccess ? SPENSE_OK : report_hip(e);
 }
