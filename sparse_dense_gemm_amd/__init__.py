@@ -211,12 +211,13 @@ def _need_dtype(t, dtype, what: str) -> None:
 
 
 def _matrix(t, what: str):
-    """Rows, columns and row stride of a matrix that is contiguous along a row."""
+    """Rows, columns and row stride of a matrix that is contiguous along a row.  A single row's stride says nothing (of the
+    last position of a sequence it may be any number): it is taken as dense."""
     rows, cols = t.shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what} {rows} x {cols} is not contiguous along a row")
-    return rows, cols, ld
+    return rows, cols, cols if rows == 1 else ld
 
 
 def _too_small(what: str, rows: int, cols: int):
@@ -733,7 +734,7 @@ def _operand(t, rows: int, H: int, what: str):
     if step != 1 and cols > 1:
         raise ValueError(f"{what} {have} x {cols} is not contiguous along a row")
     d = _dtypes.get(t.dtype)
-    return t.data_ptr(), ld, dtype_of(t) if d is None else d
+    return t.data_ptr(), H if have == 1 else ld, dtype_of(t) if d is None else d
 
 
 def _vector(t, H: int, what: str):
