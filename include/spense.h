@@ -44,7 +44,9 @@
  *     grow them, which sizes them for every batch size up to its own, whatever
  *     split count the planner picks there (spense_linear_splits with a forced
  *     split count sizes them for that call only).  mx4, fp8b and experts' layers: any
- *     call of the same entry point with at least as many rows (see there).  The
+ *     call of the same entry point with at least as many rows (see there; the first
+ *     with more rows than any before plans every smaller number too, 0.3 to 0.6 us of
+ *     the host for each sixteen rows).  The
  *     calls record kernel launches only; the split-K hand-off counters are reset
  *     by the kernels.  Workspaces that a captured call used stay allocated until
  *     spense_free, so its graph may also be replayed after a call that needed

@@ -64,7 +64,9 @@ bool stream_weights(const Fp8bDesc& d, bool grouped, int64_t R16, const ExpertsS
 // rows of codes 36, 31, 33; 10 with fp32 out 23, 17, 30; 80 rows of codes 48, 36, 40,
 // of bf16 45, 38, 44; of 1600 x 5120, 16 rows of bf16 23, 17, 28.  One m-tile of bf16,
 // of which a CU takes two workgroups, is ahead where there are enough of them and
-// experts have two rows or fewer: 10 rows 23, 27, 29.
+// experts have two rows or fewer: 10 rows 23, 27, 29.  Against every configuration, 45
+// such layers of 4 to 700 tokens: 1.02 of the best one's time at the median, 1.14 at
+// 90%, 1.25 at worst (149 tokens of bf16, 1600 x 5120: 28.4, one m-tile 22.7).
 double plan_cycles(const Fp8bDesc& d, bool grouped, Fp8bKind kind, int config, int64_t S, double groups, int64_t hit,
                    int64_t R) {
   const ExpertsShape c = fp8b_shape(kind, config);

@@ -12,6 +12,11 @@
 // at 5120 columns, and few rows would leave the chip empty).  Bound by memory: 8191
 // rows of 5120 (bf16 in, residual and gate in fp32 and bf16, codes out) 99 us, 464 MB
 // at 4.7 TB/s; 2048 rows of 5120, each the sum of two fp32 rows, 28 us, 147 MB at 5.3.
+// Above 6144 columns a CU holds one workgroup, whose loads, barriers and stores
+// nothing covers: 7168, 8192 and 27648 columns 107, 104 and 110 us for the same bytes,
+// and the sums of 8192 and 12288 columns 30 and 40 (four pieces a thread, of which the
+// sums of fp32 rows spill 36 to 116 bytes a lane; so does an fp32 residual with bf16
+// rows of a length that is no multiple of eight, 36 bytes).
 // One row takes 3.0 us, most of it the launch and the wait for its loads.
 #include <algorithm>
 #include <cfloat>
