@@ -615,7 +615,7 @@ def _fp8b_strides(codes, scales, M: int, K: int, rows: int):
     """Row strides of an fp8b matrix of at least M x K, its blocks `rows` rows high."""
     crows, ccols, ldc = _matrix(codes, "codes")
     srows, scols, lds = _matrix(scales, "scales")
-    if codes.element_size() != 1:
+    if codes.element_size() != 1 or (codes.is_floating_point() and codes.dtype is not _torch().float8_e4m3fn):
         raise TypeError(f"codes are bytes (uint8 or float8_e4m3fn), not {codes.dtype}")
     if scales.dtype is not _torch().float32:
         _need_dtype(scales, _torch().float32, "scales")
