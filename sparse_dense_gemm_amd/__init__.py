@@ -212,12 +212,14 @@ def _need_dtype(t, dtype, what: str) -> None:
 
 def _matrix(t, what: str):
     """Rows, columns and row stride of a matrix that is contiguous along a row.  A single row's stride says nothing (of the
-    last position of a sequence it may be any number): it is taken as dense."""
+    last position of a sequence it may be any number): one that no row of a matrix could have is taken as dense."""
     rows, cols = t.shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what} {rows} x {cols} is not contiguous along a row")
-    return rows, cols, cols if rows == 1 else ld
+    if rows == 1 and not cols <= ld < 1 << 22:
+        ld = cols
+    return rows, cols, ld
 
 
 def _too_small(what: str, rows: int, cols: int):

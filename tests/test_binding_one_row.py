@@ -78,3 +78,11 @@ def test_norm(calls, i):
     sdg.spense_block_norm(O, wide, wide[:, :K], None, eps=1e-6, stream=0)
     call = sdg.NormCall.from_buffer_copy(calls.pop()[1][0])
     assert call.ldr == call.ldro == K and call.residual == call.residual_out
+
+
+def test_an_ordinary_stride_stays(calls):
+    """A padded row's stride, which may be what lets it be read in place."""
+    X = torch.zeros((1, 264), dtype=torch.bfloat16)[:, :K + 3]
+    off = torch.zeros(2, dtype=torch.int32)
+    sdg._experts_linear(1, DIMS, X, off, torch.zeros((1, N)), None, sdg.DT_BF16, None, 0)
+    assert 264 in calls.pop()[1]
