@@ -212,7 +212,8 @@ def _need_dtype(t, dtype, what: str) -> None:
 
 def _matrix(t, what: str):
     """Rows, columns and row stride of a matrix that is contiguous along a row.  A single row's stride says nothing (of the
-    last position of a sequence it may be any number): one that no row of a matrix could have is taken as dense."""
+    last position of a sequence it may be any number): below its length, or from 2^22 on, where the layers lay rows out
+    or refuse them, the row is taken as dense."""
     rows, cols = t.shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
