@@ -332,8 +332,12 @@ int spense_quantize_tokens(const void* X, int64_t M, int64_t K, int64_t ldx, uin
  * writes them in the layer's packed column order (the dense-set permutation
  * rides on the quantisation, as the SlideSparse explainer folds its activation
  * re-ordering into per-token quantisation), into the handle's workspace.
- * Products of two e4m3 values are exact in fp32; the sum runs in fp32 in a
- * fixed order (bitwise repeatable).
+ * Products of two e4m3 values are exact in fp32.  The matrix instructions on codes add
+ * several of them at a time and drop what lies more than 13 bits below the largest
+ * of those, whatever the type of Y; the rest of the sum runs in fp32, in a fixed
+ * order (bitwise repeatable).  So the sum may be off by 2^-10 of sum_k |Xq Wp|, besides
+ * its fp32 roundings: far less on ordinary inputs, but where large products cancel
+ * more than the result's own rounding.  spense_linear on the layer keeps all bits.
  *
  *   h      an input-split layer packed from SPENSE_FP8_E4M3 weights
  *          (SPENSE_EUNSUPPORTED for other weight types and for output-split
